@@ -292,6 +292,136 @@ i8l_status int8_linear_backward_weight(const uint16_t *X, const uint16_t *dY, in
                                        int64_t K, int64_t N, uint16_t *dW, uint16_t *dbias,
                                        void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Serving in 8 bits around the layer --------------------------------------
+ * What a decoder layer does between its quantized linear layers, with the 8-bit
+ * data kept as codes: the norm that feeds a product with row codes, the product
+ * of codes that are already there, a key/value cache held in 8 bits, and
+ * attention over it.  16-bit tensors are fp16 or bf16 (i8l_dtype), passed as
+ * raw bits. */
+typedef enum { I8L_FP16 = 0, I8L_BF16 = 1 } i8l_dtype;
+
+/* Residual addition, root-mean-square norm and row codes:
+ *   h = round16(X + residual)   (X itself without a residual),
+ *   g = h * weight,  a[i] = max_k |g[i][k]|,
+ *   Xq = clamp(round_half_away(g * fl32(127 / a)), -127, 127)   (0 where a is 0),
+ *   sx = a / sqrt(mean_k h^2 + eps),
+ * so that Xq * sx / 127 is the norm's value: the operands of int8_linear_codes.
+ * The factor 1 / rms is common to the row and enters the scale alone.
+ *   X         [M][K]  dtype, 16-byte aligned
+ *   residual  [M][K]  dtype, or NULL
+ *   weight    [K]     dtype, or NULL (ones)
+ *   h         [M][K]  out, or NULL (not stored); may be X or residual
+ *   Xq        int8 [M][K] out; sx fp32 [M] out
+ *   eps       >= 0
+ * Statistics in fp32.  A row with a non-finite h or g gets the scale NaN (or
+ * infinity where only g overflowed).  M and K as for int8_linear. */
+i8l_status int8_rmsnorm_quant(const uint16_t *X, const uint16_t *residual,
+                              const uint16_t *weight, int64_t M, int64_t K, float eps,
+                              int dtype, int8_t *Xq, float *sx, uint16_t *h, void *stream);
+
+/* Workspace bytes of int8_linear_codes for this shape (0: none needed). */
+size_t i8l_codes_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/* Product of row codes with a quantized weight, no outlier columns:
+ *   Y = fp16(acc * sx[i] * sw[n] / 127^2 + bias[n]),  acc = sum_k Xq[i][k] Wq[n][k],
+ * acc exact in int32, one rounding (to nearest even, overflow to infinity).
+ *   Xq  int8 [M][K] and sx fp32 [M], e.g. from int8_rmsnorm_quant
+ *   Wq, sw  from int8_quantize_weight;  bias fp16 [N] or NULL
+ *   workspace  device scratch, 16-byte aligned, or NULL: without one of
+ *              i8l_codes_workspace_bytes the last partial round of tiles is not
+ *              split along K (same result).  A smaller one: I8L_ERR_WORKSPACE.
+ * Shapes, alignment and errors as for int8_linear. */
+i8l_status int8_linear_codes(const int8_t *Xq, const float *sx, int64_t M, int64_t K,
+                             const int8_t *Wq, const float *sw, int64_t N, const uint16_t *bias,
+                             uint16_t *Y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* A key/value cache in 8 bits, in pages of page_size tokens; keys and values
+ * have one scale for each page and kv head.
+ *   scale = fl32(absmax / 127) over the page's page_size * head_dim values,
+ *   code = clamp(round_half_away(x * fl32(127 / absmax)), -127, 127),
+ *   value = code * scale   (a page with a NaN or an infinity: scale NaN).
+ * A page's codes are made when its last token arrives; the tokens of a
+ * sequence's last, incomplete page are kept in 16 bits in the sequence's slot.
+ * So no value is rounded twice, and what the cache holds does not depend on how
+ * many calls wrote it.  The caller owns the memory and hands out pages. */
+typedef struct {
+  int8_t *k_codes;    /* [n_pages][heads][page_size][head_dim], 16-byte aligned */
+  int8_t *v_codes;    /* [n_pages][heads][head_dim][page_size], 16-byte aligned */
+  float *k_scale;     /* [n_pages][heads] */
+  float *v_scale;     /* [n_pages][heads] */
+  uint16_t *k_tail;   /* [n_slots][heads][page_size][head_dim] dtype, 16-byte aligned */
+  uint16_t *v_tail;   /* [n_slots][heads][head_dim][page_size] dtype, 16-byte aligned */
+  int64_t n_pages, n_slots;
+  int32_t heads;      /* kv heads, 1 .. 4096 */
+  int32_t head_dim;   /* a multiple of 16, 16 .. 256 */
+  int32_t page_size;  /* 16, 32, 64 or 128 */
+  int32_t dtype;      /* i8l_dtype of the tails and of the 16-bit tensors */
+} i8l_kv_cache;
+
+/* The sequences of a call (device arrays).  Entries are clamped to what the
+ * tensors hold: a page or slot outside the cache is neither read nor written
+ * (its tokens are skipped; attention masks them), a length past
+ * max_pages * page_size ends there. */
+typedef struct {
+  const int32_t *page_table;  /* [n][max_pages]: page of tokens i * page_size .. */
+  const int32_t *lengths;     /* [n]: tokens of each sequence, this call's included */
+  const int32_t *cu;          /* [n + 1], ascending: sequence i has rows cu[i] .. cu[i+1] - 1
+                                 of the call's packed tensors; NULL: row i alone */
+  const int32_t *slots;       /* [n]: its tail slot; NULL: slot i */
+  int32_t n;                  /* sequences, 0 .. 65535 */
+  int32_t max_pages;          /* max_pages * page_size < 2^30 */
+} i8l_sequences;
+
+/* Writes the call's rows as the last tokens of their sequences: row j of a
+ * sequence with m rows is its token lengths[i] - m + j.  Tokens before them in
+ * the same page must be in the slot (written there by earlier calls).  Pages and
+ * slots of different sequences must differ.
+ *   k, v   [rows][heads][head_dim] dtype; element (t, h, d) at
+ *          t * token_stride + h * head_stride + d (strides in elements,
+ *          multiples of 8; pointers 16-byte aligned)
+ *   max_new  at least the rows of any one sequence */
+i8l_status int8_cache_write(const i8l_kv_cache *cache, const i8l_sequences *seqs,
+                            const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride,
+                            const uint16_t *v, int64_t v_token_stride, int64_t v_head_stride,
+                            int64_t rows, int64_t max_new, void *stream);
+
+/* Reads sequences back: rows cu[i] .. cu[i] + lengths[i] - 1 of k and v
+ * [rows][heads][head_dim] (dtype, contiguous, 16-byte aligned) receive the
+ * tokens of sequence i, complete pages as round16(code * scale), the rest as
+ * written.  cu is required.
+ *   max_len  at least the longest sequence */
+i8l_status int8_cache_read(const i8l_kv_cache *cache, const i8l_sequences *seqs, uint16_t *k,
+                           uint16_t *v, int64_t rows, int64_t max_len, void *stream);
+
+/* Workspace bytes of int8_cache_attention for these sizes (0: none needed, or
+ * sizes that the call refuses). */
+size_t i8l_attention_workspace_bytes(const i8l_kv_cache *cache, int64_t n, int64_t q_heads,
+                                     int64_t max_q, int64_t max_len, int64_t window);
+
+/* Causal attention of a call's queries over the cache, which already holds the
+ * keys and values of the queries' own tokens (int8_cache_write comes first): row
+ * j of a sequence with m rows is the query of token i = lengths - m + j and sees
+ * the tokens max(0, i - window + 1) .. i (window 0: all up to i):
+ *   out = softmax_t(scale * q . k_t - alibi[head] * (i - t)) . v_t,
+ * with the cache's 8-bit values (16-bit in the tail).  Query head h reads kv
+ * head h / (q_heads / heads).  A query that sees no token gives 0.
+ *   q      [rows][q_heads][head_dim] dtype; element (t, h, d) at
+ *          t * token_stride + h * head_stride + d (multiples of 8)
+ *   alibi  fp32 [q_heads] slopes, or NULL
+ *   out    [rows][q_heads][head_dim] dtype, contiguous, 16-byte aligned
+ *   max_q  at least the rows of any one sequence (rows past it are not written)
+ *   max_len  the longest sequence (sizes the split of the keys; results do
+ *          not depend on it beyond the order of sums)
+ *   workspace  i8l_attention_workspace_bytes(...) bytes, 16-byte aligned
+ * Scores, softmax statistics and sums in fp32; the weights are rounded to
+ * dtype, relative to the row's largest contribution, for the matrix cores. */
+i8l_status int8_cache_attention(const i8l_kv_cache *cache, const i8l_sequences *seqs,
+                                const uint16_t *q, int64_t q_token_stride,
+                                int64_t q_head_stride, int64_t q_heads, int64_t rows,
+                                int64_t max_q, int64_t max_len, float scale, int64_t window,
+                                const float *alibi, uint16_t *out, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char *i8l_last_error(void);
 

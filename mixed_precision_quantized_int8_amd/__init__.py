@@ -34,12 +34,34 @@ __all__ = [
     "quantize_activation_zp",
     "backward_input",
     "backward_weight",
+    "rmsnorm_quant",
+    "linear_codes",
+    "KVCache",
+    "new_cache",
+    "cache_write",
+    "cache_read",
+    "cache_attention",
+    "attention_workspace_bytes",
     "workspace_layout",
     "workspace_bytes",
     "workspace_views",
     "Int8LinError",
     "build_info",
 ]
+
+# the serving operators import torch with the module; loaded on first use
+_SERVING = ("rmsnorm_quant", "linear_codes", "KVCache", "new_cache", "cache_write", "cache_read",
+            "cache_attention", "attention_workspace_bytes")
+
+
+def __getattr__(name):
+    if name in _SERVING:
+        from . import serving
+
+        for n in _SERVING:
+            globals()[n] = getattr(serving, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

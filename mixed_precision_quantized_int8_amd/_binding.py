@@ -40,6 +40,13 @@ EXPORTS = (
     "i8l_backward_weight_workspace_bytes",
     "int8_linear_backward_input",
     "int8_linear_backward_weight",
+    "int8_rmsnorm_quant",
+    "i8l_codes_workspace_bytes",
+    "int8_linear_codes",
+    "int8_cache_write",
+    "int8_cache_read",
+    "i8l_attention_workspace_bytes",
+    "int8_cache_attention",
     "i8l_last_error",
     "i8l_build_info",
 )
@@ -65,6 +72,38 @@ class WorkspaceLayout(ctypes.Structure):
         ("gemm_slices", ctypes.c_size_t),
         ("zero_points", ctypes.c_size_t),
         ("act_partials", ctypes.c_size_t),
+    ]
+
+
+class KVCacheStruct(ctypes.Structure):
+    """i8l_kv_cache"""
+
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("k_tail", ctypes.c_void_p),
+        ("v_tail", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class SequencesStruct(ctypes.Structure):
+    """i8l_sequences"""
+
+    _fields_ = [
+        ("page_table", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("cu", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("n", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
     ]
 
 
@@ -112,6 +151,22 @@ def lib() -> ctypes.CDLL:
     L.int8_linear_backward_input.restype = ctypes.c_int
     L.int8_linear_backward_weight.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
     L.int8_linear_backward_weight.restype = ctypes.c_int
+    L.int8_rmsnorm_quant.argtypes = [vp, vp, vp, i64, i64, f32, ctypes.c_int, vp, vp, vp, vp]
+    L.int8_rmsnorm_quant.restype = ctypes.c_int
+    L.i8l_codes_workspace_bytes.argtypes = [i64, i64, i64]
+    L.i8l_codes_workspace_bytes.restype = sz
+    L.int8_linear_codes.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, vp, vp, sz, vp]
+    L.int8_linear_codes.restype = ctypes.c_int
+    cache, seqs = ctypes.POINTER(KVCacheStruct), ctypes.POINTER(SequencesStruct)
+    L.int8_cache_write.argtypes = [cache, seqs, vp, i64, i64, vp, i64, i64, i64, i64, vp]
+    L.int8_cache_write.restype = ctypes.c_int
+    L.int8_cache_read.argtypes = [cache, seqs, vp, vp, i64, i64, vp]
+    L.int8_cache_read.restype = ctypes.c_int
+    L.i8l_attention_workspace_bytes.argtypes = [cache, i64, i64, i64, i64, i64]
+    L.i8l_attention_workspace_bytes.restype = sz
+    L.int8_cache_attention.argtypes = [cache, seqs, vp, i64, i64, i64, i64, i64, i64, f32, i64, vp,
+                                       vp, vp, sz, vp]
+    L.int8_cache_attention.restype = ctypes.c_int
     L.i8l_last_error.argtypes = []
     L.i8l_last_error.restype = ctypes.c_char_p
     L.i8l_build_info.argtypes = []

@@ -41,6 +41,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "serve.h"
 
 namespace i8l {
 
@@ -1050,6 +1051,19 @@ hipError_t launch_decode_zp(const uint16_t* X, int M, int K, const int8_t* Wq, c
   hipError_t e = launch_quantize_activation(X, M, K, threshold, enabled, ws, stream, true);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(stream_kernel(M), grid, block, 0, stream, d);
+  return hipGetLastError();
+}
+
+// Codes that are already there: the streaming kernel alone, with no outlier column
+// (zeros: the count and the first indices, all 0).
+hipError_t launch_stream_codes(const int8_t* Xq, const float* sx, int M, int K, const int8_t* Wq,
+                               const float* sw, int N, const uint16_t* bias, uint16_t* Y,
+                               const int32_t* zeros, hipStream_t stream) {
+  DecodeArgs d{nullptr, M, K, N, Wq, sw, nullptr, bias, 0x10000u, Y, const_cast<int32_t*>(zeros),
+               const_cast<int32_t*>(zeros), const_cast<float*>(sx), const_cast<int8_t*>(Xq),
+               nullptr};
+  hipLaunchKernelGGL(stream_kernel(M), dim3((N + kDecCols - 1) / kDecCols), dim3(kDecThreads), 0,
+                     stream, d);
   return hipGetLastError();
 }
 

@@ -14,6 +14,7 @@
 
 #include "../../include/int8lin.h"
 #include "launch.h"
+#include "serve.h"
 
 #define I8L_API extern "C" __attribute__((visibility("default")))
 
@@ -468,6 +469,11 @@ I8L_API i8l_status int8_linear_backward_weight(const uint16_t* X, const uint16_t
 }
 
 I8L_API const char* i8l_last_error(void) { return g_err; }
+
+char* i8l::error_buffer(size_t* bytes) {
+  *bytes = sizeof(g_err);
+  return g_err;
+}
 
 I8L_API const char* i8l_build_info(void) {
   // built once (thread-safe static initialization), read-only afterwards
