@@ -20,9 +20,13 @@ __device__ __forceinline__ uint16_t from_f32(float f) {
   if constexpr (BF) return __builtin_bit_cast(uint16_t, (__bf16)f);
   return f2h(f);
 }
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 template <bool BF>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return (uint32_t)from_f32<BF>(a) | ((uint32_t)from_f32<BF>(b) << 16);
+__device__ __forceinline__ uint32_t pack2(float a, float b) {   // one v_cvt_pk
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  if constexpr (BF) return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2b));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
 }
 
 // D = A . B + C over 32 contraction elements, 16 x 16 (A row / B column =
@@ -36,6 +40,29 @@ __device__ __forceinline__ v4f mfma16(v4u a, v4u b, v4f c) {
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
                                                   __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// The same over 16 contraction elements, 32 x 32 (A row / B column = lane & 31,
+// elements 8 * (lane >> 5) .. +7; D column = lane & 31, register r the row
+// 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)).
+typedef float v16f32 __attribute__((ext_vector_type(16)));
+template <bool BF>
+__device__ __forceinline__ v16f32 mfma32(v4u a, v4u b, v16f32 c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, a),
+                                                   __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a),
+                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// The value of the lane 32 places away, with this lane's own.
+__device__ __forceinline__ void halves(float v, float* lo, float* hi) {
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const v2u r = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+  *lo = __builtin_bit_cast(float, (uint32_t)r[0]);
+  *hi = __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
 // Two dwords of int8 codes (8 values) to eight 16-bit floats, exactly.
@@ -56,7 +83,6 @@ __device__ __forceinline__ v4u codes8(uint32_t lo, uint32_t hi) {
                                              __builtin_bit_cast(uint32_t, f0), 0x07060302u);
       }
   } else {
-    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
     const v2h off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
     const uint32_t x[2] = {lo ^ 0x80808080u, hi ^ 0x80808080u};
 #pragma unroll
