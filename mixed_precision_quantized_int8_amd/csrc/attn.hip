@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
         s[j][e] = __builtin_amdgcn_exp2f(s[j][e] - ms);
         add += s[j][e];
       }
-    if (add != 0.0f) l = __builtin_fmaf(add, inv_vs, l);   // (no 0 * NaN of a masked page)
+    l = __builtin_fmaf(add, inv_vs, l);
   };
   auto weights = [&](const v4f (&s)[4], int st) -> v4u {   // contraction step st
     v4u p;
@@ -213,7 +213,9 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
     const bool all = t0 >= lo_last && t0 + kAdTile <= min(hi_first, coded) && !__any(pv < 0);
     float base = __builtin_amdgcn_logf(vs);
     if (ALIBI) base = __builtin_fmaf(slope, (float)(tv - pos), base);
-    soften(s, sc * ks, base, 1.0f / vs, t0, all, lo, min(hi, coded), pv >= 0);
+    // a page of NaNs: its weights are NaN where they are seen, 0 where they are not
+    const float inv_vs = vs < __builtin_inff() ? 1.0f / vs : 0.0f;
+    soften(s, sc * ks, base, inv_vs, t0, all, lo, min(hi, coded), pv >= 0);
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       const v4u p = weights(s, st);
@@ -331,9 +333,9 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
 constexpr int kApTile = 64;
 constexpr float kApSlack = 8.0f;
 
-template <bool BF, int DP, int NW, bool ALIBI>
-__global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
-  constexpr int NT = 64 * NW;
+template <bool BF, int DP, int NW, int RB, bool ALIBI>
+__global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(AttnArgs a) {
+  constexpr int NT = 64 * NW, kRows = 32 * NW * RB;
   constexpr int NK = DP / 16;               // contraction steps of Q . K
   constexpr int ND = DP / 32;               // 32-row blocks of O^T
   constexpr int CH = 4 * DP;                // 16-code chunks of a tile of keys, and of values
@@ -357,26 +359,33 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
   const int n_rows = sq.n * G;
   // the last rows see the most keys: they go first
   const int tiles = (int)gridDim.x / H;
-  const int r_wg = (tiles - 1 - (int)blockIdx.x / H) * 32 * NW;
+  const int r_wg = (tiles - 1 - (int)blockIdx.x / H) * kRows;
   if (r_wg >= n_rows) return;
   const int first_pos = sq.len - sq.n;      // position of query 0
 
-  // this lane's query; rows past the end repeat the last
-  const int r_wave = r_wg + 32 * wave;
-  const bool live = r_wave + l32 < n_rows;
-  const int rr = min(r_wave + l32, n_rows - 1);
-  const int qi = rr / G, qg = rr % G;
-  const int pos = first_pos + qi;
-  const int hi = min(pos + 1, sq.len);
-  const int lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+  // this lane's queries, one in each of the wave's RB blocks of 32 rows; rows past
+  // the end repeat the last
+  const int r_wave = r_wg + 32 * RB * wave;
+  int lo[RB], hi[RB], pos[RB], qi[RB], qg[RB];
+  bool live[RB];
+#pragma unroll
+  for (int w = 0; w < RB; ++w) {
+    const int r = r_wave + 32 * w + l32;
+    live[w] = r < n_rows;
+    qi[w] = min(r, n_rows - 1) / G;
+    qg[w] = min(r, n_rows - 1) % G;
+    pos[w] = first_pos + qi[w];
+    hi[w] = min(pos[w] + 1, sq.len);
+    lo[w] = a.window > 0 ? max(0, pos[w] + 1 - a.window) : 0;
+  }
   auto low = [&](int row) -> int {   // first key that a row sees
     const int p = first_pos + row / G;
     return a.window > 0 ? max(0, p + 1 - a.window) : 0;
   };
   auto high = [&](int row) -> int { return min(first_pos + row / G + 1, sq.len); };
-  const int wv0 = min(r_wave, n_rows - 1), wv1 = min(r_wave + 31, n_rows - 1);
-  const int wv_lo1 = low(wv1), wv_hi0 = high(wv0);   // what every row of the wave sees
-  const int wg_lo = low(r_wg), wg_hi = high(min(r_wg + 32 * NW, n_rows) - 1);
+  // what every row of the wave sees, and what some row of the workgroup does
+  const int wv_lo1 = low(min(r_wave + 32 * RB, n_rows) - 1), wv_hi0 = high(min(r_wave, n_rows - 1));
+  const int wg_lo = low(r_wg), wg_hi = high(min(r_wg + kRows, n_rows) - 1);
 
   const int coded = sq.len >> ps << ps;
   const int first = wg_lo & ~127;
@@ -386,24 +395,29 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
   const int c_end = min(end, coded);
   const int n_coded = c_end > c_begin ? (c_end - c_begin + kApTile - 1) / kApTile : 0;
   const int n_tail = end > coded && coded >= begin ? (end - coded + kApTile - 1) / kApTile : 0;
-  const int n_tiles = n_coded + n_tail;
 
-  v4u qf[NK];
+  v4u qf[RB][NK];
+  float slope[RB];
 #pragma unroll
-  for (int s = 0; s < NK; ++s) {
-    const int d = 16 * s + 8 * hf;
-    qf[s] = v4u{0, 0, 0, 0};
-    if (live && d < D)
-      qf[s] = *reinterpret_cast<const v4u*>(a.q + (sq.c0 + qi) * a.q_ts + (h * G + qg) * a.q_hs + d);
+  for (int w = 0; w < RB; ++w) {
+#pragma unroll
+    for (int s = 0; s < NK; ++s) {
+      const int d = 16 * s + 8 * hf;
+      qf[w][s] = v4u{0, 0, 0, 0};
+      if (live[w] && d < D)
+        qf[w][s] = *reinterpret_cast<const v4u*>(a.q + (sq.c0 + qi[w]) * a.q_ts +
+                                                 (h * G + qg[w]) * a.q_hs + d);
+    }
+    slope[w] = ALIBI ? a.alibi[h * G + qg[w]] * kLog2e : 0.0f;
   }
   const float sc = a.scale * kLog2e;
-  const float slope = ALIBI ? a.alibi[h * G + qg] * kLog2e : 0.0f;
 
   // ---- staging -----------------------------------------------------------------
+  // No branches: a key past the coded ones repeats the last page, a page that the
+  // cache does not have reads page 0, an element past D the page's start; the
+  // group's base, the zeros of q and the rows of O that nobody stores hide them.
   const int32_t* table = a.s.table + (size_t)b * a.s.max_pages;
   const size_t page_sz = (size_t)P * D;
-  // as the table has it (looked at when it is used, a step later); -1: none
-  auto page_at = [&](int tok) -> int { return tok < coded ? table[tok >> ps] : -1; };
   auto exists = [&](int page) { return (uint32_t)page < (uint32_t)a.c.n_pages; };
   // chunk u of this thread: keys (rows of D codes) first, then values (rows of P);
   // its place within a page and its group of 16 keys do not change from tile to
@@ -411,293 +425,387 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
   auto is_k = [&](int u) { return t + u * NT < CH; };
   const int8_t* at0[CPT];   // the chunk in page 0
   int sub[CPT];             // its keys' offset in the tile, a multiple of 16
-  bool use[CPT];
+  uint32_t place[CPT];      // byte offset of its first 16-byte piece in a buffer (the
+                            // second: exchanged, ^ 16)
 #pragma unroll
   for (int u = 0; u < CPT; ++u) {
     const int c = t + u * NT;
     const int key = is_k(u) ? c / (DP / 16) : ((c - CH) & 3) * 16;
     const int d = is_k(u) ? c % (DP / 16) * 16 : (c - CH) >> 2;
     sub[u] = key & ~15;
-    use[u] = d < D;
-    at0[u] = (is_k(u) ? a.c.kc : a.c.vc) + h * page_sz +
-             (is_k(u) ? (key & (P - 1)) * D + d : d * P + (key & (P - 1)));
+    at0[u] = (is_k(u) ? a.c.kc : a.c.vc) + h * page_sz;
+    if (d < D) at0[u] += is_k(u) ? (key & (P - 1)) * D + d : d * P + (key & (P - 1));
+    place[u] = is_k(u) ? key * DP * 2 + (((d >> 3) ^ (key & KMASK)) << 4)
+                       : kKeys + d * kApTile * 2 + (((key >> 3) ^ ((d >> 1) & 7)) << 4);
   }
   const uint32_t page_step = (uint32_t)(H * page_sz);   // at most 4096 * 128 * 256
+  // A thread's value chunks run one tile behind its key chunks: step j takes keys of
+  // tile j and values of tile j - 1.
+  auto tile_of = [&](int u, int j) { return is_k(u) ? j : j - 1; };
   int pg[CPT];          // pages of the chunks to load next
   v4u raw[CPT];         // codes in flight
-  int pm = -1;          // threads 0 .. 3: the page of 16-key group t
+  auto load_page = [&](int u, int j) {
+    pg[u] = table[min(c_begin + max(tile_of(u, j), 0) * kApTile + sub[u], coded - 1) >> ps];
+  };
+  auto load_chunk = [&](int u, int j) {   // after load_page(u, j)
+    const int in_page = (c_begin + tile_of(u, j) * kApTile) & (P - 1) & kApTile;
+    const uint32_t page = exists(pg[u]) ? (uint32_t)pg[u] : 0u;
+    raw[u] = *reinterpret_cast<const v4u*>(at0[u] + (uint64_t)page * page_step +
+                                           (is_k(u) ? in_page * D : in_page));
+  };
+  auto store_piece = [&](int u, int w, int j) {   // piece w of chunk u
+    *reinterpret_cast<v4u*>(s_kv + (((uint32_t)(tile_of(u, j) & 1) * kBuf + place[u]) ^ (16 * w))) =
+        codes8<BF>(raw[u][2 * w], raw[u][2 * w + 1]);
+  };
+  // lanes 0 .. 3 of wave 0: page and scales of 16-key group `lane` of a tile
+  int pm = -1;
   float ks = 0.0f, vs = 0.0f;
+  auto load_meta_page = [&](int i) {
+    const int tok = c_begin + i * kApTile + 16 * lane;
+    pm = tok < coded ? table[tok >> ps] : -1;
+  };
   bool meta_ok = false;
-  // a thread's value chunks run one tile behind its key chunks (see the loop):
-  // step j takes keys of tile j and values of tile j - 1
-  auto tile_of = [&](int u, int j) { return is_k(u) ? j : j - 1; };
-  auto load_pages = [&](int j) {
-#pragma unroll
-    for (int u = 0; u < CPT; ++u) {
-      const int i = tile_of(u, j);
-      pg[u] = i >= 0 && i < n_coded ? page_at(c_begin + i * kApTile + sub[u]) : -1;
-    }
-    pm = j < n_coded && t < 4 ? page_at(c_begin + j * kApTile + 16 * t) : -1;
-  };
-  auto load_codes = [&](int j) {   // after load_pages(j)
-#pragma unroll
-    for (int u = 0; u < CPT; ++u) {
-      const int in_page = (c_begin + tile_of(u, j) * kApTile) & (P - 1) & kApTile;
-      raw[u] = v4u{0, 0, 0, 0};
-      if (exists(pg[u]) && use[u])
-        raw[u] = *reinterpret_cast<const v4u*>(at0[u] + (uint64_t)(uint32_t)pg[u] * page_step +
-                                               (is_k(u) ? in_page * D : in_page));
-    }
+  auto load_scales = [&]() {
     meta_ok = exists(pm);
-    if (meta_ok) {
-      ks = a.c.ks[(size_t)pm * H + h];
-      vs = a.c.vs[(size_t)pm * H + h];
-    }
+    const size_t f = (size_t)(meta_ok ? pm : 0) * H + h;
+    ks = a.c.ks[f];
+    vs = a.c.vs[f];
   };
-  // byte offset of this thread's first piece of chunk u in its buffer; the second
-  // piece is its neighbour (16 bytes, exchanged: ^ 16)
-  auto place = [&](int u) -> uint32_t {
-    const int c = t + u * NT;
-    if (is_k(u)) {
-      const int key = c / (DP / 16), p = c % (DP / 16) * 2;
-      return (uint32_t)(key * DP * 2 + ((p ^ (key & KMASK)) << 4));
-    }
-    const int d = (c - CH) >> 2, p = ((c - CH) & 3) * 2;
-    return (uint32_t)(kKeys + d * kApTile * 2 + ((p ^ ((d >> 1) & 7)) << 4));
-  };
-  auto put = [&](int i, int u, v4u x, v4u y) {
-    const uint32_t at = (uint32_t)(i & 1) * kBuf + place(u);
-    *reinterpret_cast<v4u*>(s_kv + at) = x;
-    *reinterpret_cast<v4u*>(s_kv + (at ^ 16)) = y;
-  };
-  auto key0 = [&](int i) { return i < n_coded ? c_begin + i * kApTile : coded + (i - n_coded) * kApTile; };
-  // step j into LDS: keys and scales of tile j, values of tile j - 1
-  auto store = [&](int j) {
-#pragma unroll
-    for (int u = 0; u < CPT; ++u) {
-      const int i = tile_of(u, j);
-      if (i < 0 || i >= n_coded) continue;   // (uniform in a wave)
-      put(i, u, codes8<BF>(raw[u][0], raw[u][1]), codes8<BF>(raw[u][2], raw[u][3]));
-    }
-    if (t < 4 && j < n_coded) {
-      const float v = vs == 0.0f ? kZeroScale : vs < kLeastScale ? kLeastScale : vs;
-      s_mul[j & 1][t] = meta_ok ? sc * ks : 0.0f;
-      s_base[j & 1][t] = meta_ok ? __builtin_amdgcn_logf(v) : -__builtin_inff();   // hides the group
-      s_inv[j & 1][t] = meta_ok ? 1.0f / v : 0.0f;
-    }
-    // keys coded + 64 j .. of the incomplete page, as they are; past the length zeros
-    if (j >= n_coded && j - 1 < n_tiles) {
-      const int slot = a.s.slots ? a.s.slots[b] : b;
-      const bool ok = slot >= 0 && slot < a.c.n_slots;
-      const size_t f = ((size_t)(ok ? slot : 0) * H + h) * page_sz;
-#pragma unroll
-      for (int u = 0; u < CPT; ++u) {
-        const int i = tile_of(u, j), c = t + u * NT;
-        if (i < n_coded || i >= n_tiles) continue;
-        const int t0 = key0(i), r0 = t0 - coded, n = ok ? min(sq.len - t0, kApTile) : 0;
-        v4u x[2];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {   // two 16-byte pieces
-          x[w] = v4u{0, 0, 0, 0};
-          if (is_k(u)) {
-            const int key = c / (DP / 16), p = c % (DP / 16) * 2 + w;
-            if (key < n && p * 8 < D)
-              x[w] = *reinterpret_cast<const v4u*>(a.c.kt + f + (size_t)(r0 + key) * D + p * 8);
-          } else {
-            const int d = (c - CH) >> 2, p = ((c - CH) & 3) * 2 + w, nv = n - p * 8;
-            if (nv > 0 && d < D)
-              x[w] = *reinterpret_cast<const v4u*>(a.c.vt + f + (size_t)d * P + r0 + p * 8);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              x[w][q] &= (2 * q < nv ? 0xffffu : 0u) | (2 * q + 1 < nv ? 0xffff0000u : 0u);
-          }
-        }
-        put(i, u, x[0], x[1]);
-      }
-      if (t < 4 && j < n_tiles) {
-        s_mul[j & 1][t] = ok ? sc : 0.0f;
-        s_base[j & 1][t] = ok ? 0.0f : -__builtin_inff();
-        s_inv[j & 1][t] = ok ? 1.0f : 0.0f;
-      }
-    }
+  auto store_meta = [&](int i, bool ok, float kscale, float vscale) {
+    const float v = vscale == 0.0f ? kZeroScale : vscale < kLeastScale ? kLeastScale : vscale;
+    s_mul[i & 1][lane] = ok ? sc * kscale : 0.0f;
+    s_base[i & 1][lane] = ok ? __builtin_amdgcn_logf(v) : -__builtin_inff();   // hides the group
+    // a page of NaNs: its weights are NaN where they are seen, 0 where they are not
+    s_inv[i & 1][lane] = ok && v < __builtin_inff() ? 1.0f / v : 0.0f;
   };
 
-  // ---- a tile ------------------------------------------------------------------
-  float m = -__builtin_inff(), l = 0.0f;   // l: this lane's keys
-  v16f32 o[ND];
+  // ---- half a tile, 32 keys -------------------------------------------------------
+  // maximum (0 until a key is seen: then limit is -inf) and sum (of this lane's keys)
+  float m[RB], limit[RB], l[RB];
+  v16f32 s[2][RB], o[RB][ND];
+  v4u p[RB][2];
 #pragma unroll
-  for (int d = 0; d < ND; ++d) o[d] = v16f32{};
+  for (int w = 0; w < RB; ++w) {
+    m[w] = l[w] = 0.0f;
+    limit[w] = -__builtin_inff();
+    p[w][0] = p[w][1] = v4u{0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[w][d] = v16f32{};
+  }
   const int row_k = (l32 & 0x13) | ((l32 & 4) << 1) | ((l32 & 8) >> 1);   // key of score row l32
-
-  v16f32 s[2];
-  v4u p[4];
-  // S^T of one tile and O^T of the one before it (either may be left out): the
-  // fragments come from LDS kAhead products before their use, in program order
-  auto multiply = [&](auto with_k, auto with_v, int ik, int iv) {
-    constexpr int nk = decltype(with_k)::value ? 2 * NK : 0;
-    constexpr int nv = decltype(with_v)::value ? 4 * ND : 0;
-    constexpr int kAhead = 6;
-    // offsets of the first fragments; the others differ in a constant and in the
-    // piece's number, exchanged.  (Opaque: the sums are made here, not kept.)
-    uint32_t ak = (uint32_t)(ik & 1) * kBuf + row_k * DP * 2 + ((hf ^ (row_k & KMASK)) << 4);
-    uint32_t av = (uint32_t)(iv & 1) * kBuf + kKeys + l32 * kApTile * 2 + ((hf ^ ((l32 >> 1) & 7)) << 4);
-    asm volatile("" : "+v"(ak), "+v"(av));
-    auto fragment = [&](int n) -> v4u {
-      if (n < nk)
-        return *reinterpret_cast<const v4u*>(s_kv + (ak ^ ((n >> 1) << 5)) + (n & 1) * 32 * DP * 2);
-      const int g = (n - nk) / ND, d = (n - nk) % ND;
-      return *reinterpret_cast<const v4u*>(s_kv + (av ^ (g << 5)) + d * 32 * kApTile * 2);
-    };
+  // LDS offsets of this lane's first fragments: the others differ in a constant and
+  // in the piece's number, exchanged
+  const uint32_t at_k = (uint32_t)(row_k * DP * 2 + ((hf ^ (row_k & KMASK)) << 4));
+  const uint32_t at_v = (uint32_t)(kKeys + l32 * kApTile * 2 + ((hf ^ ((l32 >> 1) & 7)) << 4));
+  auto frag_k = [&](uint32_t at, int u, int k) {   // step u of Q . K, half k
+    return *reinterpret_cast<const v4u*>(s_kv + (at ^ (u << 5)) + k * 32 * DP * 2);
+  };
+  auto frag_v = [&](uint32_t at, int n, int k) {   // 16 keys 2 k + n / ND, block n % ND
+    return *reinterpret_cast<const v4u*>(s_kv + (at ^ ((2 * k + n / ND) << 5)) +
+                                         (n % ND) * 32 * kApTile * 2);
+  };
+  v4f mul, base0, inv;   // of the tile at hand
+  float top[RB];
+  // Register 8 g + e of s[k]: key 32 k + 16 g + 8 hf + e.  Pair j of block w (two
+  // neighbours): scores less the maximum so far, and the highest of them;
+  float bias[RB][2];
+  auto bias_of = [&](int t0, int k, int w, int g) {
+    const float x = base0[2 * k + g] - m[w];
+    return ALIBI ? __builtin_fmaf(slope[w], (float)(t0 + 32 * k + 16 * g + 8 * hf - pos[w]), x) : x;
+  };
+  auto shift = [&](int k, int w, int j) {
+#pragma unroll
+    for (int e = 2 * j; e < 2 * j + 2; ++e) {
+      float x = __builtin_fmaf(s[k][w][e], mul[2 * k + (e >> 3)], bias[w][e >> 3]);
+      if (ALIBI) x = __builtin_fmaf(slope[w], (float)(e & 7), x);
+      s[k][w][e] = x;
+      top[w] = __builtin_fmaxf(top[w], x);
+    }
+  };
+  // scores to weights in 16 bits, and their sum.
+  float add[RB][2];
+  auto weigh = [&](int k, int w, int j) {
+    const float w0 = __builtin_amdgcn_exp2f(s[k][w][2 * j]);
+    const float w1 = __builtin_amdgcn_exp2f(s[k][w][2 * j + 1]);
+    uint32_t pair = pack2<BF>(w0, w1);
+    asm volatile("" : "+v"(pair));   // formed in its slot, not next to its use
+    p[w][j >> 2][j & 3] = pair;
+    add[w][j >> 2] += w0 + w1;
+  };
+  auto total = [&](int k) {
+#pragma unroll
+    for (int w = 0; w < RB; ++w)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) l[w] = __builtin_fmaf(add[w][g], inv[2 * k + g], l[w]);
+  };
+  // masks the scores where a row of the wave does not see a key; moves the maximum
+  auto settle = [&](int tile0, int k) {
+    const int t0 = tile0 + 32 * k;
+    if (!(t0 >= wv_lo1 && t0 + 32 <= wv_hi0)) {   // uniform
+#pragma unroll
+      for (int w = 0; w < RB; ++w) {
+        top[w] = -__builtin_inff();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int key = t0 + 16 * (r >> 3) + 8 * hf + (r & 7);
+          const float x = key >= lo[w] && key < hi[w] ? s[k][w][r] : -__builtin_inff();
+          s[k][w][r] = x;
+          top[w] = __builtin_fmaxf(top[w], x);
+        }
+      }
+    }
+    bool move = false;
+#pragma unroll
+    for (int w = 0; w < RB; ++w) move |= top[w] > limit[w];
+    if (__any(move)) {
+#pragma unroll
+      for (int w = 0; w < RB; ++w) {
+        float a0, a1;   // both halves of the wave hold the same queries
+        halves(top[w], &a0, &a1);
+        const float high = __builtin_fmaxf(a0, a1);
+        const bool fresh = limit[w] < 0.0f, some = high > -__builtin_inff();
+        // the maximum moves by `up` (at first from nothing, to the tile's)
+        const float up = some ? (fresh ? high : __builtin_fmaxf(high, 0.0f)) : 0.0f;
+        const float f = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up);
+        m[w] += up;
+        if (some) limit[w] = kApSlack;
+        l[w] *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[w][d] *= f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[k][w][r] -= up;
+      }
+    }
+  };
+  // Half k of tile i.  A wave issues in order, so the matrix cores and the vector
+  // unit work at once only where their instructions alternate: the products of the
+  // outputs of the half tile before with the shifts of this one's scores, then the
+  // products of the next half tile's scores with this one's weights, in slots of
+  // one product and its share of the vector work.  Fragments are read kAhead steps
+  // before their use; `extra(n)` is more vector work for the first NV slots.
+  constexpr int kAhead = 4, NV = 2 * ND, kPairs = 8 / NK;   // pairs of a block per slot
+  auto half_tile = [&](int i, int k, auto extra) {
+    const int t0 = c_begin + i * kApTile;
+    uint32_t av = at_v + (uint32_t)((k ? i : i - 1) & 1) * kBuf;
+    uint32_t ak = at_k + (uint32_t)((k ? i + 1 : i) & 1) * kBuf;
+    asm volatile("" : "+v"(av), "+v"(ak));   // (offsets are formed here, not kept)
+    auto fragment = [&](int n) { return n < NV ? frag_v(av, n, k ^ 1) : frag_k(ak, n - NV, k ^ 1); };
     v4u f[kAhead];
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) f[n] = fragment(n);
-    if constexpr (nk > 0) s[0] = s[1] = v16f32{};
 #pragma unroll
-    for (int n = 0; n < nk + nv; ++n) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (n < nk) s[n & 1] = mfma32<BF>(f[n % kAhead], qf[n >> 1], s[n & 1]);
-      else o[(n - nk) % ND] = mfma32<BF>(f[n % kAhead], p[(n - nk) / ND], o[(n - nk) % ND]);
-      if (n + kAhead < nk + nv) f[n % kAhead] = fragment(n + kAhead);
+    for (int w = 0; w < RB; ++w) {
+      top[w] = -__builtin_inff();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) bias[w][g] = bias_of(t0, k, w, g);
+    }
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+#pragma unroll
+      for (int w = 0; w < RB; ++w) {
+        __builtin_amdgcn_sched_barrier(0);
+        o[w][n % ND] = mfma32<BF>(f[n % kAhead], p[w][n / ND], o[w][n % ND]);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) shift(k, w, n * kPairs + j);
+      }
+      f[n % kAhead] = fragment(n + kAhead);
+      extra(n);
     }
     __builtin_amdgcn_sched_barrier(0);
-  };
-  auto soften = [&](int i) {   // S^T to weights
-    // register 8 w + e of block k: key 32 k + 16 w + 8 hf + e; scores less the maximum
-    const int t0 = key0(i);
-    const v4f mul = *reinterpret_cast<const v4f*>(s_mul[i & 1]);
-    const v4f base0 = *reinterpret_cast<const v4f*>(s_base[i & 1]);
-    const v4f inv = *reinterpret_cast<const v4f*>(s_inv[i & 1]);
-    const float m0 = m == -__builtin_inff() ? 0.0f : m;
-    float top = -__builtin_inff();
-    auto scores = [&](auto all) {
+    settle(t0, k);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float base = base0[g] - m0;
-        if (ALIBI) base = __builtin_fmaf(slope, (float)(t0 + 16 * g + 8 * hf - pos), base);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float x = __builtin_fmaf(s[g >> 1][8 * (g & 1) + e], mul[g], base);
-          if (ALIBI) x = __builtin_fmaf(slope, (float)e, x);
-          if constexpr (!decltype(all)::value) {
-            const int k = t0 + 16 * g + 8 * hf + e;
-            x = k >= lo && k < hi ? x : -__builtin_inff();
-          }
-          s[g >> 1][8 * (g & 1) + e] = x;
-          top = __builtin_fmaxf(top, x);
-        }
-      }
-    };
-    // every row of the wave sees every key of the tile, or not
-    if (t0 >= wv_lo1 && t0 + kApTile <= wv_hi0) scores(std::true_type{});
-    else scores(std::false_type{});
-    float t_lo, t_hi;
-    halves(top, &t_lo, &t_hi);
-    top = __builtin_fmaxf(t_lo, t_hi);
-    const bool fresh = m == -__builtin_inff();
-    if (__any(top > kApSlack || (fresh && top > -__builtin_inff()))) {
-      // the maximum moves: by `up` (at first from nothing, to the tile's)
-      const float up = fresh ? (top == -__builtin_inff() ? 0.0f : top) : __builtin_fmaxf(top, 0.0f);
-      const float f = __builtin_amdgcn_exp2f(-up);
-      if (!fresh) {
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[d] *= f;
-        m += up;
-      } else if (top > -__builtin_inff()) {
-        m = up;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        s[0][e] -= up;
-        s[1][e] -= up;
-      }
+    for (int w = 0; w < RB; ++w) {
+      add[w][0] = add[w][1] = 0.0f;
+      s[k ^ 1][w] = v16f32{};
     }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float add = 0.0f;
+    for (int n = NV; n < NV + NK; ++n) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float w0 = __builtin_amdgcn_exp2f(s[g >> 1][8 * (g & 1) + 2 * u]);
-        const float w1 = __builtin_amdgcn_exp2f(s[g >> 1][8 * (g & 1) + 2 * u + 1]);
-        p[g][u] = pack2<BF>(w0, w1);
-        add += w0 + w1;
+      for (int w = 0; w < RB; ++w) {
+        __builtin_amdgcn_sched_barrier(0);
+        s[k ^ 1][w] = mfma32<BF>(f[n % kAhead], qf[w][n - NV], s[k ^ 1][w]);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) weigh(k, w, (n - NV) * kPairs + j);
       }
-      // (a hidden page's scale may be NaN: no 0 * NaN)
-      l = __builtin_fmaf(add, add != 0.0f ? inv[g] : 0.0f, l);
+      if (n + kAhead < NV + NK) f[n % kAhead] = fragment(n + kAhead);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    total(k);
+  };
+
+  auto load_meta = [&](int i) {
+    mul = *reinterpret_cast<const v4f*>(s_mul[i & 1]);
+    base0 = *reinterpret_cast<const v4f*>(s_base[i & 1]);
+    inv = *reinterpret_cast<const v4f*>(s_inv[i & 1]);
+  };
+  auto first_scores = [&](int i, int k) {
+    const uint32_t at = at_k + (uint32_t)(i & 1) * kBuf;
+#pragma unroll
+    for (int w = 0; w < RB; ++w) s[k][w] = v16f32{};
+#pragma unroll
+    for (int u = 0; u < NK; ++u) {
+      const v4u f = frag_k(at, u, k);
+#pragma unroll
+      for (int w = 0; w < RB; ++w) s[k][w] = mfma32<BF>(f, qf[w][u], s[k][w]);
+    }
+  };
+  auto last_outputs = [&](int i, int k) {
+    const uint32_t at = at_v + (uint32_t)(i & 1) * kBuf;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const v4u f = frag_v(at, n, k);
+#pragma unroll
+      for (int w = 0; w < RB; ++w) o[w][n % ND] = mfma32<BF>(f, p[w][n / ND], o[w][n % ND]);
     }
   };
 
-  // ---- the loop ----------------------------------------------------------------
-  // Step i of a wave: the matrix part, S of tile i and O of tile i - 1, then the
-  // vector part, the weights of tile i and its share of the staging.  With eight
-  // waves, two on each SIMD, waves 4 .. 7 run half a step behind waves 0 .. 3, so
-  // that on every SIMD one wave's matrix part goes with the other's vector part;
-  // a barrier ends every half step.  The early waves then stage keys of tile
-  // i + 1 and values of tile i, the late ones a tile further: no buffer is
-  // written while it is read, and each is whole a half step before its first use.
-  if (n_tiles > 0) {
-    constexpr bool kPair = NW == 8;
-    const bool late = kPair && wave >= 4;
-    const int ahead = late ? 2 : 1;
-    for (int j = 0; j < ahead; ++j) {
-      load_pages(j);
-      load_codes(j);
-      store(j);
+  // ---- the loop over complete pages ----------------------------------------------
+  // Step i + 1 (keys of tile i + 1, values of tile i) goes to LDS in the first half
+  // of tile i and is read from the second half on; what the first half still reads,
+  // keys of tile i and values of tile i - 1, is in the other buffers.
+  if (n_coded > 0) {
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) load_page(u, 0);
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) load_chunk(u, 0);
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) load_page(u, 1);
+    const bool meta = t < 4;
+    if (meta) {
+      load_meta_page(0);
+      load_scales();
+      load_meta_page(1);
     }
-    load_pages(ahead);
-    load_codes(ahead);
-    load_pages(ahead + 1);
+#pragma unroll
+    for (int u = 0; u < CPT; ++u)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!is_k(u)) raw[u] = v4u{0, 0, 0, 0};   // values of tile -1, multiplied by no weight
+        store_piece(u, w, 0);
+      }
+    if (meta) {
+      store_meta(0, meta_ok, ks, vs);
+      load_scales();
+      load_meta_page(2);
+    }
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) load_chunk(u, 1);
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) load_page(u, 2);
     lds_sync();
-    if (late) lds_sync();
-    multiply(std::true_type{}, std::false_type{}, 0, 0);
-    for (int i = 0; i < n_tiles; ++i) {
-      if (kPair) lds_sync();
-      store(i + ahead);
-      load_codes(i + ahead + 1);
-      load_pages(i + ahead + 2);
-      soften(i);
+    first_scores(0, 0);
+    for (int i = 0; i < n_coded; ++i) {
+      load_meta(i);
+      if (meta) {
+        store_meta(i + 1, meta_ok, ks, vs);
+        load_scales();
+        load_meta_page(i + 3);
+      }
+      // the staging in the first slots: convert and store step i + 1, load step i + 2
+      half_tile(i, 0, [&](int n) {
+        constexpr int kPer = (4 * CPT + NV - 1) / NV;   // units a slot
+#pragma unroll
+        for (int x = n * kPer; x < (n + 1) * kPer; ++x) {
+          if (x < 2 * CPT) store_piece(x / 2, x % 2, i + 1);
+          else if (x < 3 * CPT) load_chunk(x - 2 * CPT, i + 2);
+          else if (x < 4 * CPT) load_page(x - 3 * CPT, i + 3);
+        }
+      });
       lds_sync();
-      // (after the last tile the scores are of whatever the buffer holds, and unused)
-      multiply(std::true_type{}, std::true_type{}, i + 1, i);
+      // (past the last tile the scores are of whatever the buffer holds, and unused)
+      half_tile(i, 1, [](int) {});
     }
-    if (kPair && !late) lds_sync();
+    last_outputs(n_coded - 1, 1);
+  }
+  // ---- the keys of the incomplete page, 16 bits each, a tile at a time -------------
+  for (int j = 0; j < n_tail; ++j) {
+    const int t0 = coded + j * kApTile, r0 = j * kApTile;
+    const int slot = a.s.slots ? a.s.slots[b] : b;
+    const bool ok = slot >= 0 && slot < a.c.n_slots;
+    const size_t f = ((size_t)(ok ? slot : 0) * H + h) * page_sz;
+    const int n = ok ? min(sq.len - t0, kApTile) : 0;
+    lds_sync();   // buffer 0 has been read
+    for (int c = t; c < kApTile * DP / 8; c += NT) {
+      const int key = c / (DP / 8), piece = c % (DP / 8);
+      v4u x = {0, 0, 0, 0};
+      if (key < n && piece * 8 < D)
+        x = *reinterpret_cast<const v4u*>(a.c.kt + f + (size_t)(r0 + key) * D + piece * 8);
+      *reinterpret_cast<v4u*>(s_kv + key * DP * 2 + ((piece ^ (key & KMASK)) << 4)) = x;
+    }
+    for (int c = t; c < DP * kApTile / 8; c += NT) {   // past the length: zeros
+      const int d = c >> 3, piece = c & 7, nv = n - piece * 8;
+      v4u x = {0, 0, 0, 0};
+      if (nv > 0 && d < D)
+        x = *reinterpret_cast<const v4u*>(a.c.vt + f + (size_t)d * P + r0 + piece * 8);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        x[q] &= (2 * q < nv ? 0xffffu : 0u) | (2 * q + 1 < nv ? 0xffff0000u : 0u);
+      *reinterpret_cast<v4u*>(s_kv + kKeys + d * kApTile * 2 + ((piece ^ ((d >> 1) & 7)) << 4)) = x;
+    }
+    if (t < 4) store_meta(0, ok, 1.0f, 1.0f);
+    lds_sync();
+    load_meta(0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      first_scores(0, k);
+#pragma unroll
+      for (int w = 0; w < RB; ++w) {
+        top[w] = -__builtin_inff();
+        add[w][0] = add[w][1] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) bias[w][g] = bias_of(t0, k, w, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) shift(k, w, e);
+      }
+      settle(t0, k);
+#pragma unroll
+      for (int w = 0; w < RB; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) weigh(k, w, e);
+      total(k);
+      last_outputs(0, k);
+    }
   }
 
-  float l_lo, l_hi;
-  halves(l, &l_lo, &l_hi);
-  l = l_lo + l_hi;
-  if (!live) return;
-  const int64_t row_out = (sq.c0 + qi) * H * G + h * G + qg;
-  if (a.n_split == 1) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // no key at all: 0
+#pragma unroll
+  for (int w = 0; w < RB; ++w) {
+    float l_lo, l_hi;
+    halves(l[w], &l_lo, &l_hi);
+    const float sum = l_lo + l_hi;
+    if (!live[w]) continue;
+    if (a.n_split == 1) {
+      const int64_t row_out = (sq.c0 + qi[w]) * H * G + h * G + qg[w];
+      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key at all: 0
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int at = 32 * d + 8 * q + 4 * hf;
+          if (at < D) {
+            uint2 x;
+            x.x = pack2<BF>(o[w][d][4 * q] * f, o[w][d][4 * q + 1] * f);
+            x.y = pack2<BF>(o[w][d][4 * q + 2] * f, o[w][d][4 * q + 3] * f);
+            *reinterpret_cast<uint2*>(a.out + row_out * D + at) = x;
+          }
+        }
+      continue;
+    }
+    const size_t row = ((size_t)b * H + h) * ((size_t)G * a.max_q) + r_wave + 32 * w + l32;
+    const size_t at = row * a.n_split + split;
+    const size_t n_part = (size_t)a.s.B * H * G * a.max_q * a.n_split;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int at = 32 * d + 8 * q + 4 * hf;
-        if (at < D) {
-          uint2 w;
-          w.x = pack2<BF>(o[d][4 * q] * inv, o[d][4 * q + 1] * inv);
-          w.y = pack2<BF>(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv);
-          *reinterpret_cast<uint2*>(a.out + row_out * D + at) = w;
-        }
+        const int e = 32 * d + 8 * q + 4 * hf;
+        if (e < D)
+          *reinterpret_cast<v4f*>(a.part + 2 * n_part + at * D + e) =
+              v4f{o[w][d][4 * q], o[w][d][4 * q + 1], o[w][d][4 * q + 2], o[w][d][4 * q + 3]};
       }
-    return;
-  }
-  const size_t at = (((size_t)b * H + h) * ((size_t)G * a.max_q) + rr) * a.n_split + split;
-  const size_t n_part = (size_t)a.s.B * H * G * a.max_q * a.n_split;
-#pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e = 32 * d + 8 * q + 4 * hf;
-      if (e < D)
-        *reinterpret_cast<v4f*>(a.part + 2 * n_part + at * D + e) =
-            v4f{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
+    if (hf == 0) {
+      a.part[2 * at] = limit[w] < 0.0f ? -__builtin_inff() : m[w];
+      a.part[2 * at + 1] = sum;
     }
-  if (hf == 0) {
-    a.part[2 * at] = m;
-    a.part[2 * at + 1] = l;
   }
 }
 
@@ -770,12 +878,12 @@ void launch_kernel(const AttnArgs& a, const Plan& p, hipStream_t stream) {
     else hipLaunchKernelGGL((attn_decode_kernel<BF, 256, ALIBI>), grid, block, 0, stream, a);
   } else if (p.rows == 128) {
     if (D <= 64)
-      hipLaunchKernelGGL((attn_run_kernel<BF, 64, 4, ALIBI>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 4, ALIBI>), grid, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((attn_run_kernel<BF, 64, 4, 1, ALIBI>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 4, 1, ALIBI>), grid, dim3(256), 0, stream, a);
   } else {
     if (D <= 64)
-      hipLaunchKernelGGL((attn_run_kernel<BF, 64, 8, ALIBI>), grid, dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 8, ALIBI>), grid, dim3(512), 0, stream, a);
+      hipLaunchKernelGGL((attn_run_kernel<BF, 64, 8, 1, ALIBI>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 8, 1, ALIBI>), grid, dim3(512), 0, stream, a);
   }
 }
 
