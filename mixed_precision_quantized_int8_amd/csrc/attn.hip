@@ -54,6 +54,20 @@ __device__ __forceinline__ float xsum16(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
+// Partial results of a split launch: (m, l) of every row and split, then its
+// unnormalised output (not written where l is 0 and m -infinity).
+__device__ __forceinline__ size_t part_at(const AttnArgs& a, int b, int h, int row, int split) {
+  return (((size_t)b * a.c.H + h) * ((size_t)a.G * a.max_q) + row) * a.n_split + split;
+}
+__device__ __forceinline__ float* part_out(const AttnArgs& a, size_t at) {
+  return a.part + 2 * ((size_t)a.s.B * a.c.H * a.G * a.max_q * a.n_split) + at * a.c.D;
+}
+__device__ __forceinline__ void say_empty(const AttnArgs& a, int b, int h, int row, int split) {
+  const size_t at = part_at(a, b, h, row, split);
+  a.part[2 * at] = -__builtin_inff();
+  a.part[2 * at + 1] = 0.0f;
+}
+
 // 16 rows (queries of one kv head: token-major, the G heads of a token together)
 // against a range of keys.  S^T = K . Q^T and O^T = V^T . P^T on 16x16x32
 // matrix instructions; lane l holds query l & 15, and of a tile of 64 keys the
@@ -98,6 +112,11 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
   const int end = split == a.n_split - 1 ? all_hi : min(begin + a.chunk, all_hi);
   const int coded = sq.len >> ps << ps;            // tokens in complete pages
 
+  if (begin >= end && a.n_split > 1) {   // nothing to see here: no more than that is said
+    if (t < min(16, n_rows - r0)) say_empty(a, b, h, r0 + t, split);
+    return;
+  }
+
   // query operands: elements 64 c + 16 grp + 8 s .. +7 of chunk c, step s
   v4u qf[NC][2];
 #pragma unroll
@@ -120,11 +139,6 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
 
   const int32_t* table = a.s.table + (size_t)b * a.s.max_pages;
   const size_t page_sz = (size_t)P * D;
-  auto page_at = [&](int tok) -> int {   // -1: none
-    const int g = tok >> ps;
-    const int p = g < a.s.max_pages ? table[g] : -1;
-    return p >= 0 && p < a.c.n_pages ? p : -1;
-  };
 
   // scores of one tile (scaled, in log2 units, base included) to weights, the
   // running maximum and sum; then O
@@ -178,28 +192,62 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
     return p;
   };
 
-  auto coded_tile = [&](int t0) {
-    const int tk = t0 + 16 * (i16 >> 2), tv = t0 + 16 * grp;   // this lane's keys as K row, as P
-    const int pk = tk < coded ? page_at(tk) : -1, pv = tv < coded ? page_at(tv) : -1;
-    const size_t fk = (size_t)max(pk, 0) * H + h, fv = (size_t)max(pv, 0) * H + h;
-    const int8_t* kp = a.c.kc + fk * page_sz + (size_t)((tk & (P - 1)) + (i16 & 3)) * D + 16 * grp;
-    const int8_t* vp = a.c.vc + fv * page_sz + (size_t)i16 * P + (tv & (P - 1));
-    v4u kb[4][NC], vb[ND];
+  // Complete pages: tile i of this wave starts at key c0 + 256 i.  The registers of
+  // a tile's keys are free once its scores are formed, those of its values once its
+  // outputs are: each then takes the next tile's codes, so that half a tile or more
+  // is on its way at any time; the page numbers come a tile before that.
+  const int c0 = max(begin, lo_first & ~(kAdTile - 1)) + wave * kAdTile;
+  const int c_end = min(end, coded);
+  const int sub_k = 16 * (i16 >> 2), sub_v = 16 * grp;   // this lane's keys as K row, as P
+  const int8_t* k_at = a.c.kc + h * page_sz + (size_t)(((sub_k & (P - 1)) + (i16 & 3)) * D + 16 * grp);
+  const int8_t* v_at = a.c.vc + h * page_sz + (size_t)(i16 * P + (sub_v & (P - 1)));
+  const uint32_t page_step = (uint32_t)(H * page_sz);   // at most 4096 * 128 * 256
+  int pk = 0, pv = 0;          // pages of the tile to load next, as the table has them
+  v4u kb[4][NC], vb[ND];       // codes
+  float ks = 0.0f, vs0 = 0.0f;
+  bool page_ok = false;
+  auto load_pages = [&](int t0) {   // (keys past the coded ones: any entry, hidden below)
+    pk = table[min((t0 + sub_k) >> ps, a.s.max_pages - 1)];
+    pv = table[min((t0 + sub_v) >> ps, a.s.max_pages - 1)];
+  };
+  auto exists = [&](int page) { return (uint32_t)page < (uint32_t)a.c.n_pages; };
+  auto load_k = [&](int t0) {
+    const int8_t* p = k_at + (uint64_t)(exists(pk) ? (uint32_t)pk : 0u) * page_step +
+                      (t0 & (P - 1) & kAdTile) * D;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        kb[j][c] = v4u{0, 0, 0, 0};
-        if (64 * c + 16 * grp < D)
-          kb[j][c] = *reinterpret_cast<const v4u*>(kp + 4 * j * D + 64 * c);
-      }
+      for (int c = 0; c < NC; ++c)   // an element past D meets a zero of q
+        if (D > 64 * c) {            // uniform
+          const int8_t* q = 64 * c + 16 * grp < D ? p + 64 * c : p;
+          kb[j][c] = *reinterpret_cast<const v4u*>(q + 4 * j * D);
+        }
+  };
+  auto load_v = [&](int t0) {
+    page_ok = exists(pv);
+    const uint32_t page = page_ok ? (uint32_t)pv : 0u;
+    ks = a.c.ks[(size_t)page * H + h];
+    vs0 = a.c.vs[(size_t)page * H + h];
+    const int8_t* p = v_at + (uint64_t)page * page_step + (t0 & (P - 1) & kAdTile);
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      vb[d] = v4u{0, 0, 0, 0};
-      if (16 * d < D) vb[d] = *reinterpret_cast<const v4u*>(vp + (size_t)16 * d * P);
-    }
-    const float ks = a.c.ks[fv], vs0 = a.c.vs[fv];
-    const float vs = vs0 == 0.0f ? kZeroScale : vs0 < kLeastScale ? kLeastScale : vs0;
+    for (int d = 0; d < ND; ++d)
+      if (16 * d < D) vb[d] = *reinterpret_cast<const v4u*>(p + (size_t)16 * d * P);   // uniform
+  };
+  // (no entry of the table depends on the length: the first ones leave with it)
+  load_pages(c0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) kb[j][c] = v4u{0, 0, 0, 0};
+#pragma unroll
+  for (int d = 0; d < ND; ++d) vb[d] = v4u{0, 0, 0, 0};
+  if (c0 < c_end) {
+    load_k(c0);
+    load_v(c0);
+    load_pages(c0 + kAdWaves * kAdTile);
+  }
+  for (int t0 = c0; t0 < c_end; t0 += kAdWaves * kAdTile) {
+    const int next = t0 + kAdWaves * kAdTile;
     v4f s[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -210,12 +258,15 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
         for (int st = 0; st < 2; ++st)
           s[j] = mfma16<BF>(codes8<BF>(kb[j][c][2 * st], kb[j][c][2 * st + 1]), qf[c][st], s[j]);
     }
-    const bool all = t0 >= lo_last && t0 + kAdTile <= min(hi_first, coded) && !__any(pv < 0);
+    if (next < c_end) load_k(next);
+    const int tv = t0 + sub_v;
+    const float vs = vs0 == 0.0f ? kZeroScale : vs0 < kLeastScale ? kLeastScale : vs0;
+    const bool all = t0 >= lo_last && t0 + kAdTile <= min(hi_first, coded) && !__any(!page_ok);
     float base = __builtin_amdgcn_logf(vs);
     if (ALIBI) base = __builtin_fmaf(slope, (float)(tv - pos), base);
     // a page of NaNs: its weights are NaN where they are seen, 0 where they are not
     const float inv_vs = vs < __builtin_inff() ? 1.0f / vs : 0.0f;
-    soften(s, sc * ks, base, inv_vs, t0, all, lo, min(hi, coded), pv >= 0);
+    soften(s, sc * ks, base, inv_vs, t0, all, lo, min(hi, coded), page_ok);
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       const v4u p = weights(s, st);
@@ -223,7 +274,11 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
       for (int d = 0; d < ND; ++d)
         o[d] = mfma16<BF>(codes8<BF>(vb[d][2 * st], vb[d][2 * st + 1]), p, o[d]);
     }
-  };
+    if (next < c_end) {
+      load_v(next);
+      load_pages(next + kAdWaves * kAdTile);
+    }
+  }
 
   // keys of the incomplete page, 16 bits each; values past the length are
   // whatever the slot held before and are cleared
@@ -268,11 +323,9 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
     }
   };
 
-  for (int t0 = begin + wave * kAdTile; t0 < end; t0 += kAdWaves * kAdTile) {
-    if (t0 + kAdTile <= lo_first) continue;
-    if (t0 < coded) coded_tile(t0);
-    if (t0 + kAdTile > coded) tail_tile(t0);
-  }
+  if (end > coded && coded >= begin)
+    for (int t0 = (coded & ~(kAdTile - 1)) + wave * kAdTile; t0 < end; t0 += kAdWaves * kAdTile)
+      tail_tile(t0);
 
   // the four waves' results together
   l = xsum16(l);
@@ -309,9 +362,8 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
       w.y = pack2<BF>(oo[2] * inv, oo[3] * inv);
       *reinterpret_cast<uint2*>(a.out + ((sq.c0 + i) * H * G + h * G + g) * (int64_t)D + d) = w;
     } else {
-      const size_t at = (((size_t)b * H + h) * ((size_t)G * a.max_q) + R) * a.n_split + split;
-      const size_t n_part = (size_t)a.s.B * H * G * a.max_q * a.n_split;
-      *reinterpret_cast<v4f*>(a.part + 2 * n_part + at * D + d) = oo;
+      const size_t at = part_at(a, b, h, R, split);
+      *reinterpret_cast<v4f*>(part_out(a, at) + d) = oo;
       if (d == 0) {
         a.part[2 * at] = mm;
         a.part[2 * at + 1] = ll;
@@ -391,6 +443,10 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
   const int first = wg_lo & ~127;
   const int begin = first + split * a.chunk;
   const int end = split == a.n_split - 1 ? wg_hi : min(begin + a.chunk, wg_hi);
+  if (begin >= end && a.n_split > 1) {   // nothing to see here: no more than that is said
+    for (int r = t; r < min(kRows, n_rows - r_wg); r += NT) say_empty(a, b, h, r_wg + r, split);
+    return;
+  }
   const int c_begin = max(begin, wg_lo & ~(kApTile - 1));
   const int c_end = min(end, coded);
   const int n_coded = c_end > c_begin ? (c_end - c_begin + kApTile - 1) / kApTile : 0;
@@ -790,16 +846,14 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
         }
       continue;
     }
-    const size_t row = ((size_t)b * H + h) * ((size_t)G * a.max_q) + r_wave + 32 * w + l32;
-    const size_t at = row * a.n_split + split;
-    const size_t n_part = (size_t)a.s.B * H * G * a.max_q * a.n_split;
+    const size_t at = part_at(a, b, h, r_wave + 32 * w + l32, split);
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int e = 32 * d + 8 * q + 4 * hf;
         if (e < D)
-          *reinterpret_cast<v4f*>(a.part + 2 * n_part + at * D + e) =
+          *reinterpret_cast<v4f*>(part_out(a, at) + e) =
               v4f{o[w][d][4 * q], o[w][d][4 * q + 1], o[w][d][4 * q + 2], o[w][d][4 * q + 3]};
       }
     if (hf == 0) {
@@ -809,7 +863,8 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
   }
 }
 
-// The splits of one row together: one wave per row.
+// The splits of one row together: one wave per row.  Lane s weighs split s; the
+// outputs of eight splits are on their way at a time.
 template <bool BF>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, h = blockIdx.y, b = blockIdx.z;
@@ -817,25 +872,42 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const Rows sq = rows_of(a, b);
   if (R >= sq.n * a.G) return;
   const int H = a.c.H, D = a.c.D;
-  const size_t at = (((size_t)b * H + h) * ((size_t)a.G * a.max_q) + R) * a.n_split;
-  const size_t n_part = (size_t)a.s.B * H * a.G * a.max_q * a.n_split;
+  const size_t at = part_at(a, b, h, R, 0);
   const float* ml = a.part + 2 * at;
-  const float* po = a.part + 2 * n_part + at * D;
+  const float* po = part_out(a, at);
   float m = -__builtin_inff();
   for (int s = lane; s < a.n_split; s += 64) m = __builtin_fmaxf(m, ml[2 * s]);
   m = wave_max(m);
   const float ms = m == -__builtin_inff() ? 0.0f : m;
   float l = 0.0f;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // elements lane + 64 u
+  for (int s0 = 0; s0 < a.n_split; s0 += 64) {
+    float f = 0.0f;
+    if (s0 + lane < a.n_split) {
+      f = __builtin_amdgcn_exp2f(ml[2 * (s0 + lane)] - ms);
+      l = __builtin_fmaf(ml[2 * (s0 + lane) + 1], f, l);
+    }
+    const int n = min(64, a.n_split - s0);
+    for (int j = 0; j < n; j += 8) {
+      float fj[8], x[8][4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        fj[e] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), j + e));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)   // (an empty split has no output)
+          x[e][u] = fj[e] != 0.0f && 64 * u < D && lane + 64 * u < D
+                        ? po[(size_t)(s0 + j + e) * D + lane + 64 * u]
+                        : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[u] = __builtin_fmaf(x[e][u], fj[e], acc[u]);
+    }
+  }
+  for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off, 64);
   const int i = R / a.G, g = R % a.G;
   uint16_t* out = a.out + ((sq.c0 + i) * H * a.G + h * a.G + g) * (int64_t)D;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // elements lane + 64 u
-  for (int s = 0; s < a.n_split; ++s) {
-    const float f = __builtin_amdgcn_exp2f(ml[2 * s] - ms);
-    l = __builtin_fmaf(ml[2 * s + 1], f, l);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (lane + 64 * u < D) acc[u] = __builtin_fmaf(po[(size_t)s * D + lane + 64 * u], f, acc[u]);
-  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int u = 0; u < 4; ++u)
@@ -859,7 +931,7 @@ Plan plan(int B, int H, int G, int D, int max_q, int max_len, int window) {
   const int64_t tiles = heads * ((rows + p.rows - 1) / p.rows);
   // at least 256 keys a workgroup; about four workgroups a compute unit (single
   // rows), or one (runs)
-  const int64_t want = std::max<int64_t>((p.rows == 16 ? 1024 : 256) / tiles, 1);
+  const int64_t want = std::max<int64_t>((p.rows == 16 ? 4096 : 512) / tiles, 1);
   const int64_t c = std::max<int64_t>(((range + want - 1) / want + 255) / 256 * 256, 256);
   p.chunk = (int)c;
   p.n_split = std::max((int)((range + c - 1) / c), 1);
