@@ -327,9 +327,9 @@ size_t i8l_codes_workspace_bytes(int64_t M, int64_t K, int64_t N);
  * acc exact in int32, one rounding (to nearest even, overflow to infinity).
  *   Xq  int8 [M][K] and sx fp32 [M], e.g. from int8_rmsnorm_quant
  *   Wq, sw  from int8_quantize_weight;  bias fp16 [N] or NULL
- *   workspace  device scratch, 16-byte aligned, or NULL: without one of
- *              i8l_codes_workspace_bytes the last partial round of tiles is not
- *              split along K (same result).  A smaller one: I8L_ERR_WORKSPACE.
+ *   workspace  device scratch of i8l_codes_workspace_bytes, 16-byte aligned
+ *              (a smaller one: I8L_ERR_WORKSPACE), or NULL: then nothing is
+ *              split along K (same result, more slowly where the output is small)
  * Shapes, alignment and errors as for int8_linear. */
 i8l_status int8_linear_codes(const int8_t *Xq, const float *sx, int64_t M, int64_t K,
                              const int8_t *Wq, const float *sw, int64_t N, const uint16_t *bias,

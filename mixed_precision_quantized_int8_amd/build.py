@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libint8lin.so")
 
 ARCH = "gfx950"
 SOURCES = ["wquant.hip", "act.hip", "gemm.hip", "skinny.hip", "decode.hip", "train.hip",
-           "norm.hip", "kvcache.hip", "attn.hip", "int8lin_abi.hip", "serve_abi.hip"]
+           "norm.hip", "codes.hip", "kvcache.hip", "attn.hip", "int8lin_abi.hip", "serve_abi.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

@@ -926,12 +926,23 @@ Plan plan(int B, int H, int G, int D, int max_q, int max_len, int window) {
   int range = max_len;
   if (window > 0) range = (int)std::min((int64_t)max_len, (int64_t)window + max_q + 128);
   const int64_t rows = (int64_t)G * max_q, heads = (int64_t)B * H;
+  // Up to 16 rows are one tile of attn_decode_kernel, which reads the keys once for
+  // each 16 rows; more take attn_run_kernel, unless the whole call is so short that
+  // its longer way per tile shows (8 kv heads, 1024 keys: 128 rows 12.7 against
+  // 18.4 us, 256 rows 16.9 against 20.2, 512 rows 25.6 against 22.5).
   p.rows = 16;
-  if (rows > 16 && D <= 128) p.rows = heads * ((rows + 255) / 256) >= 256 ? 256 : 128;
+  if (rows > 16 && D <= 128 && heads * ((rows + 15) / 16) * range > (1 << 18)) {
+    // Wider tiles stage and convert a key for more rows (8 kv heads, 2048 rows over
+    // 8192 keys: 128 -> 93 us); narrow ones where the rows, or a short range, would
+    // leave compute units idle (64 heads, 512 rows over 1024 keys: 54 -> 37 us).
+    const int64_t wide = heads * ((rows + 255) / 256);
+    p.rows = rows > 128 && (wide >= 256 || range > 2048) ? 256 : 128;
+  }
+  // Splits of at least 256 keys, for about 16 (single rows: ragged lengths even out),
+  // 2 or 1 workgroups a compute unit.
   const int64_t tiles = heads * ((rows + p.rows - 1) / p.rows);
-  // at least 256 keys a workgroup; about four workgroups a compute unit (single
-  // rows), or one (runs)
-  const int64_t want = std::max<int64_t>((p.rows == 16 ? 4096 : 512) / tiles, 1);
+  const int64_t fill = p.rows == 16 ? 4096 : p.rows == 128 ? 512 : 256;
+  const int64_t want = std::max<int64_t>(fill / tiles, 1);
   const int64_t c = std::max<int64_t>(((range + want - 1) / want + 255) / 256 * 256, 256);
   p.chunk = (int)c;
   p.n_split = std::max((int)((range + c - 1) / c), 1);

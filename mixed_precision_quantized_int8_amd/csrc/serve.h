@@ -24,6 +24,26 @@ hipError_t launch_stream_codes(const int8_t* Xq, const float* sx, int M, int K, 
                                const float* sw, int N, const uint16_t* bias, uint16_t* Y,
                                const int32_t* zeros, hipStream_t stream);
 
+// Product of row codes (codes.hip): which kernel, and the partial sums it can use.
+struct CodesArgs {
+  const int8_t* Xq;
+  const float* sx;
+  const int8_t* Wq;
+  const float* sw;
+  const uint16_t* bias;   // fp16 [N] or NULL
+  uint16_t* Y;
+  int32_t* part;          // p.workspace bytes, or NULL: nothing is split along k
+  int M, N, K;
+  int n_split;            // set by the launcher
+};
+struct CodesPlan {
+  enum Kind { kStream, kRows, kTiles, kSkinny, kGemm } kind;
+  int n_split;
+  size_t workspace;       // bytes of partial sums
+};
+CodesPlan codes_plan(int M, int N, int K);
+hipError_t launch_codes(CodesArgs a, const CodesPlan& p, const int32_t* zeros, hipStream_t stream);
+
 // One cache and the sequences of a call.  Pages of P = 1 << ps tokens.
 struct Cache {
   int8_t* kc;       // [n_pages][H][P][D]

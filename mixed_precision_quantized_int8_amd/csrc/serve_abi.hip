@@ -102,14 +102,6 @@ i8l_status zero_words(const char* fn, const int32_t** out) {
   return I8L_OK;
 }
 
-// Partial tiles of the GEMM's split tail (M > kSkinnyMaxM), for up to
-// kGemmMaxSlices compute units.
-int codes_slices(int64_t M, int64_t K, int64_t N) {
-  if (M <= i8l::kSkinnyMaxM || N <= 0) return 0;
-  const i8l::GemmSplit p = i8l::gemm_split_plan((int)M, (int)N, (int)K, i8l::kGemmMaxSlices);
-  return p.split_tiles * p.S;
-}
-
 }  // namespace
 
 I8L_API i8l_status int8_rmsnorm_quant(const uint16_t* X, const uint16_t* residual,
@@ -136,7 +128,7 @@ I8L_API i8l_status int8_rmsnorm_quant(const uint16_t* X, const uint16_t* residua
 
 I8L_API size_t i8l_codes_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (check_shape("i8l_codes_workspace_bytes", M, K, N) != I8L_OK) return 0;
-  return (size_t)codes_slices(M, K, N) * 256 * 256 * sizeof(int32_t);
+  return M > 0 && N > 0 ? i8l::codes_plan((int)M, (int)N, (int)K).workspace : 0;
 }
 
 I8L_API i8l_status int8_linear_codes(const int8_t* Xq, const float* sx, int64_t M, int64_t K,
@@ -152,28 +144,20 @@ I8L_API i8l_status int8_linear_codes(const int8_t* Xq, const float* sx, int64_t 
   CHECK_PTR(sw, 4);
   CHECK_PTR(Y, 16);
   if (bias) CHECK_PTR(bias, 2);
-  int slices = 0;
+  const i8l::CodesPlan p = i8l::codes_plan((int)M, (int)N, (int)K);
   if (workspace) {
     CHECK_PTR(workspace, 16);
-    slices = codes_slices(M, K, N);
-    const size_t need = (size_t)slices * 256 * 256 * sizeof(int32_t);
-    if (workspace_bytes < need)
+    if (workspace_bytes < p.workspace)
       return fail(I8L_ERR_WORKSPACE, fn, "workspace has %zu bytes, %zu required", workspace_bytes,
-                  need);
+                  p.workspace);
   }
   const int32_t* zeros = nullptr;
   CHECK(zero_words(fn, &zeros));
   (void)hipGetLastError();
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  const int m = (int)M, k = (int)K, n = (int)N;
-  if (m <= i8l::kStreamMaxM)
-    return hip_status(fn, i8l::launch_stream_codes(Xq, sx, m, k, Wq, sw, n, bias, Y, zeros, st));
-  // X_O and idx are only read for outlier columns
-  i8l::GemmArgs g{Xq, Wq, m, n, k, sx, sw, zeros, zeros, nullptr, nullptr, Y, nullptr, bias,
-                  nullptr, nullptr, nullptr, slices ? static_cast<int32_t*>(workspace) : nullptr,
-                  slices, 0, 1};
-  if (m <= i8l::kSkinnyMaxM) return hip_status(fn, i8l::launch_gemm_skinny(g, st));
-  return hip_status(fn, i8l::launch_gemm(g, st));
+  const i8l::CodesArgs a{Xq, sx, Wq, sw, bias, Y,
+                         p.workspace ? static_cast<int32_t*>(workspace) : nullptr,
+                         (int)M, (int)N, (int)K, 1};
+  return hip_status(fn, i8l::launch_codes(a, p, zeros, static_cast<hipStream_t>(stream)));
 }
 
 // ---- The cache and attention over it ------------------------------------------------

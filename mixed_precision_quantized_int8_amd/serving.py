@@ -99,8 +99,8 @@ def linear_codes(Xq, sx, Wq, sw, bias=None, out=None, workspace=None):
 
     Xq int8 [M][K] with sx fp32 [M] (``rmsnorm_quant``), Wq int8 [N][K] with sw
     fp32 [N] (``quantize_weight``), bias fp16 [N] -> Y fp16 [M][N].  ``workspace``
-    (uint8) serves the split of a partial last round of tiles along K for more
-    than 256 rows; None allocates what the shape needs.
+    (uint8) takes the partial sums of shapes that are split along K (for more than
+    64 rows); None allocates what the shape needs.
     """
     if not isinstance(Xq, torch.Tensor) or not isinstance(Wq, torch.Tensor):
         raise TypeError("Xq and Wq must be torch.Tensors")
@@ -112,7 +112,7 @@ def linear_codes(Xq, sx, Wq, sw, bias=None, out=None, workspace=None):
     b = None if bias is None else _dense(bias, torch.float16, (N,), dev, "bias")
     if out is None:
         out = torch.empty((M, N), dtype=torch.float16, device=dev)
-    if workspace is None and M > 256:
+    if workspace is None and M > 64:
         n = int(lib().i8l_codes_workspace_bytes(M, K, N))
         workspace = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
     ws, nb = None, 0

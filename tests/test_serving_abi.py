@@ -61,7 +61,9 @@ def test_linear_codes_refusals(i8l):
         assert call(**bad) == INVALID, bad
     assert call(K=133152) == K_TOO_LARGE
     need = i8l.lib().i8l_codes_workspace_bytes(520, 2048, 1300)
-    assert need == 18 * 2 * 256 * 256 * 4   # 18 tiles, each split in two
+    assert need == 2 * 520 * 1300 * 4           # 105 tiles of 128 x 64, split in two
+    # 1344 tiles of 256 x 256: the last 64 split in four
+    assert i8l.lib().i8l_codes_workspace_bytes(2048, 14336, 43008) == 64 * 4 * 256 * 256 * 4
     assert call(M=520, K=2048, N=1300, ws=P16, n=need - 1) == WORKSPACE
     assert str(need) in i8l.last_error()
     assert L.i8l_codes_workspace_bytes(256, 4096, 16384) == 0
