@@ -198,16 +198,24 @@ __global__ __launch_bounds__(256) void codes_join_kernel(CodesArgs a) {
 CodesPlan codes_plan(int M, int N, int K) {
   CodesPlan p{CodesPlan::kGemm, 1, 0};
   if (M <= kStreamMaxM) {
-    // 64 features a workgroup fill the chip from 256 workgroups on
-    p.kind = N < 256 * 64 ? CodesPlan::kRows : CodesPlan::kStream;
+    // 16 features a workgroup until 64 of them fill the chip as well: 1 x 4096 x 8192
+    // 8.3 against 10.8 us, x 16384 14.1 against 13.0; 64 x 4096 x 4096 12.6 against
+    // 17.9, x 8192 21.5 against 18.4 (each wave reads all of the rows' codes).
+    p.kind = (int64_t)N * (M <= 16 ? 1 : 2) <= 8192 ? CodesPlan::kRows : CodesPlan::kStream;
     return p;
   }
+  // 128 x 64 tiles while 256 x 256 ones would leave three quarters of the chip idle,
+  // or half of it over a short k: 256 x 4096 x 4096 18.8 against 24.2 us (skinny
+  // tiles), x 16384 39.4 against 30.1; 1024 x 4096 x 2048 19.4 against 42.4 (256 x 256),
+  // x 4096 35.5 against 46.7, 1024 x 14336 x 4096 106 against 82.
   const int64_t wide = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
-  if (wide < 128) {
+  if (wide < 64 || (M > kSkinnyMaxM && wide < 128 && K <= 8192)) {
     p.kind = CodesPlan::kTiles;
     const int64_t tiles = (int64_t)((M + kCtM - 1) / kCtM) * ((N + kCtN - 1) / kCtN);
-    // a workgroup a compute unit; a split keeps at least four steps of k
-    const int64_t most = std::max<int64_t>((K + kCtK - 1) / kCtK / 4, 1);
+    // a workgroup a compute unit; at least four steps of k a split, and none where k is
+    // so short that the join would take longer (16 steps)
+    const int nk = (K + kCtK - 1) / kCtK;
+    const int64_t most = nk < 16 ? 1 : nk / 4;
     p.n_split = (int)std::max<int64_t>(std::min<int64_t>(256 / tiles, most), 1);
     if (p.n_split > 1) p.workspace = (size_t)p.n_split * M * N * sizeof(int32_t);
     return p;

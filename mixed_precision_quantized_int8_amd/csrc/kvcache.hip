@@ -22,7 +22,6 @@
 
 namespace i8l {
 
-constexpr int kCwThreads = 256;
 constexpr int kMaxP = 128, kMaxD = 256;
 
 struct CacheRows {
@@ -50,13 +49,47 @@ __device__ __forceinline__ Span seq_span(const Sequences& s, int b, int ps, int6
   return r;
 }
 
+// A page of one head is cut into units of 4 tokens x 8 dimensions, a thread each:
+// four 16-byte pieces of token rows on the one side, on the other 4 x 8 codes that
+// are dwords of 8 codes a token (keys) or of 4 tokens a dimension (values), so that
+// the two layouts differ by a transposition of 4 x 4 bytes in registers.  The
+// values' dwords pass through LDS, where a page is a run of 16-byte pieces with the
+// number of each exchanged by its dimension group: the threads of a wave, which hold
+// different groups of the same tokens, then write to different banks.
+//
+// BS threads, NU units each: 64 x 1 up to 256 x 4 (P * D / 32 units).
+__device__ __forceinline__ uint32_t page_piece(uint32_t c, int ps) {   // 16-byte piece number
+  return c ^ ((c >> (ps - 4) >> 3) & 7);                               // c >> (ps - 4): dimension
+}
+
+// clamp(round_half_away(x * inv), -127, 127) for |x| <= absmax as a byte in bits
+// 16 .. 23: with w = trunc(x * inv * 2^16), exact, (w + 2^15 - (w < 0)) >> 16; the
+// product of |x| <= absmax with fl32(127 / absmax) stays below 127.5, so nothing is
+// left to clamp.  (inv65: inv * 2^16.)
+__device__ __forceinline__ uint32_t code_bits(float x, float inv65) {
+  const int w = (int)(x * inv65);
+  return (uint32_t)(w + 0x8000 + (w >> 31));
+}
+
+// 4 x 4 bytes: r[e] holds bytes (token 0 .. 3) of column e from t[token] of columns.
+__device__ __forceinline__ void transpose4(const uint32_t (&t)[4], uint32_t (&r)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(t[1], t[0], 0x05010400u);   // t0.0 t1.0 t0.1 t1.1
+  const uint32_t b = __builtin_amdgcn_perm(t[3], t[2], 0x05010400u);
+  const uint32_t c = __builtin_amdgcn_perm(t[1], t[0], 0x07030602u);
+  const uint32_t d = __builtin_amdgcn_perm(t[3], t[2], 0x07030602u);
+  r[0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+  r[1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  r[2] = __builtin_amdgcn_perm(d, c, 0x05040100u);
+  r[3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
+}
+
 // One page of one head: task j of a sequence is the j-th page that its new
 // tokens touch.  Task 0 also stores the tokens that stay in the tail (after it
 // has read the tokens that were there), so no two workgroups touch one tail.
 // V: values (else keys).
-template <bool BF, bool V>
+template <bool BF, bool V, int BS, int NU>
 __device__ __forceinline__ void write_page(const Cache& c, const Sequences& s, const CacheRows& x,
-                                           int b, int h, int task, uint8_t* lds, float* red) {
+                                           int b, int h, int task, uint8_t* lds, uint32_t* red) {
   const int ps = c.ps, P = 1 << ps, D = c.D, D8 = D >> 3, t = threadIdx.x;
   const Span sp = seq_span(s, b, ps, x.rows);
   if (sp.n == 0) return;
@@ -68,66 +101,94 @@ __device__ __forceinline__ void write_page(const Cache& c, const Sequences& s, c
   const bool slot_ok = slot >= 0 && slot < c.n_slots;
   uint16_t* tail = (V ? c.vt : c.kt) + ((size_t)(slot_ok ? slot : 0) * c.H + h) * P * D;
   const uint16_t* rows = x.x[V] + h * x.hs[V];
-  // 8 elements (d8 * 8 ..) of the page's token p
-  auto load = [&](int p, int d8) -> v4u {
-    const int pos = (g << ps) + p;
-    if (pos >= p0)
-      return *reinterpret_cast<const v4u*>(rows + (sp.c0 + pos - p0) * x.ts[V] + d8 * 8);
-    v4u r = {0, 0, 0, 0};
-    if (!slot_ok) return r;
-    if (!V) return *reinterpret_cast<const v4u*>(tail + p * D + d8 * 8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      r[e >> 1] |= (uint32_t)tail[(d8 * 8 + e) * P + p] << (16 * (e & 1));
-    return r;
-  };
   if (g < full) {
     const int page = s.table[(size_t)b * s.max_pages + g];
     const bool page_ok = page >= 0 && page < c.n_pages;
-    float top = 0.0f;
-    bool bad = false;
-    for (int q = t; q < P * D8; q += kCwThreads) {
-      const v4u r = load(q / D8, q % D8);
+    const int units = (P >> 2) * D8;
+    v4u r[NU][4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = to_f32<BF>((uint16_t)(r[e >> 1] >> (16 * (e & 1))));
-        bad |= !(__builtin_fabsf(f) < __builtin_inff());
-        top = __builtin_fmaxf(top, __builtin_fabsf(f));
+    for (int u = 0; u < NU; ++u) {
+      const int q = t + u * BS, d8 = q % D8, t4 = q / D8 * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        r[u][e] = v4u{0, 0, 0, 0};
+        const int pos = (g << ps) + t4 + e;
+        if (q < units) {
+          if (pos >= p0)
+            r[u][e] = *reinterpret_cast<const v4u*>(rows + (sp.c0 + pos - p0) * x.ts[V] + d8 * 8);
+          else if (slot_ok && !V)
+            r[u][e] = *reinterpret_cast<const v4u*>(tail + (t4 + e) * D + d8 * 8);
+          else if (slot_ok)
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+              r[u][e][w >> 1] |= (uint32_t)tail[(d8 * 8 + w) * P + t4 + e] << (16 * (w & 1));
+        }
       }
     }
-    if (bad) top = __builtin_inff();
-    top = wave_max(top);
-    if ((t & 63) == 0) red[t >> 6] = top;
-    __syncthreads();
+    // magnitudes of both types are in the order of their bits, infinities and NaNs last
+    u16x2 mag = {0, 0};
 #pragma unroll
-    for (int i = 0; i < kCwThreads / 64; ++i) top = __builtin_fmaxf(top, red[i]);
-    const bool finite = top < __builtin_inff();
-    const float inv = finite ? quant_scale(top) : 0.0f;
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          mag = __builtin_elementwise_max(mag, __builtin_bit_cast(u16x2, r[u][e][w] & 0x7fff7fffu));
+    uint32_t bits = wave_max_u32(mag[0] > mag[1] ? mag[0] : mag[1]);
+    if constexpr (BS > 64) {
+      if ((t & 63) == 0) red[t >> 6] = bits;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < BS / 64; ++i) bits = max(bits, red[i]);
+    }
+    const bool finite = bits < (BF ? 0x7f80u : 0x7c00u);
+    const float top = to_f32<BF>((uint16_t)bits);
+    const float inv65 = (finite ? quant_scale(top) : 0.0f) * 65536.0f;
     int8_t* out = (V ? c.vc : c.kc) + ((size_t)(page_ok ? page : 0) * c.H + h) * P * D;
-    for (int q = t; q < P * D8; q += kCwThreads) {
-      const int p = q / D8, d8 = q % D8;
-      const v4u r = load(p, d8);
-      int k[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = to_f32<BF>((uint16_t)(r[e >> 1] >> (16 * (e & 1))));
-        k[e] = finite ? quant_code(f, inv) : 0;
-      }
+    for (int u = 0; u < NU; ++u) {
+      const int q = t + u * BS, d8 = q % D8, t4 = q / D8 * 4;
+      if (q >= units) continue;
+      uint32_t k[2][4];   // [dimensions 0 .. 3, 4 .. 7][token]
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t z[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int d = 4 * w + y;
+            const float f = to_f32<BF>((uint16_t)(r[u][e][d >> 1] >> (16 * (d & 1))));
+            z[y] = code_bits(finite ? f : 0.0f, inv65);
+          }
+          const uint32_t lo = __builtin_amdgcn_perm(z[1], z[0], 0x0c0c0602u);
+          const uint32_t hi = __builtin_amdgcn_perm(z[3], z[2], 0x06020c0cu);
+          k[w][e] = lo | hi;
+        }
       if (!V) {
-        uint2 o;
-        o.x = pack4_i8(k[0], k[1], k[2], k[3]);
-        o.y = pack4_i8(k[4], k[5], k[6], k[7]);
-        if (page_ok) *reinterpret_cast<uint2*>(out + p * D + d8 * 8) = o;
+        if (page_ok)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint2*>(out + (t4 + e) * D + d8 * 8) = make_uint2(k[0][e], k[1][e]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) lds[(d8 * 8 + e) * P + p] = (uint8_t)k[e];
+        for (int w = 0; w < 2; ++w) {
+          uint32_t y[4];
+          transpose4(k[w], y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t at = (uint32_t)(d8 * 8 + 4 * w + e) * P + t4;
+            *reinterpret_cast<uint32_t*>(lds + page_piece(at >> 4, ps) * 16 + (at & 15)) = y[e];
+          }
+        }
       }
     }
     if (V) {
       __syncthreads();
       if (page_ok)
-        for (int q = t; q < P * D / 16; q += kCwThreads)
-          *reinterpret_cast<v4u*>(out + q * 16) = *reinterpret_cast<const v4u*>(lds + q * 16);
+        for (int q = t; q < P * D / 16; q += BS)
+          *reinterpret_cast<v4u*>(out + q * 16) =
+              *reinterpret_cast<const v4u*>(lds + page_piece(q, ps) * 16);
     }
     if (t == 0 && page_ok)
       (V ? c.vs : c.ks)[(size_t)page * c.H + h] = finite ? top / 127.0f : __builtin_nanf("");
@@ -135,7 +196,7 @@ __device__ __forceinline__ void write_page(const Cache& c, const Sequences& s, c
   if (task == 0 && gl >= full && slot_ok) {   // the last page stays incomplete
     __syncthreads();   // the old tail has been read
     const int lo = max(p0, full << ps);
-    for (int q = t; q < (sp.len - lo) * D8; q += kCwThreads) {
+    for (int q = t; q < (sp.len - lo) * D8; q += BS) {
       const int pos = lo + q / D8, d8 = q % D8, p = pos & (P - 1);
       const v4u r = *reinterpret_cast<const v4u*>(rows + (sp.c0 + pos - p0) * x.ts[V] + d8 * 8);
       if (!V) {
@@ -149,15 +210,136 @@ __device__ __forceinline__ void write_page(const Cache& c, const Sequences& s, c
   }
 }
 
-template <bool BF>
-__global__ __launch_bounds__(kCwThreads) void cache_write_kernel(Cache c, Sequences s,
-                                                                 CacheRows x) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kMaxP * kMaxD];
-  __shared__ float red[kCwThreads / 64];
+template <bool BF, int BS, int NU>
+__global__ __launch_bounds__(BS) void cache_write_kernel(Cache c, Sequences s, CacheRows x) {
+  __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 32];   // a page of values
+  __shared__ uint32_t red[BS / 64];
   const int task = blockIdx.x, h = blockIdx.y >> 1, b = blockIdx.z;
-  if (blockIdx.y & 1) write_page<BF, true>(c, s, x, b, h, task, lds, red);
-  else write_page<BF, false>(c, s, x, b, h, task, lds, red);
+  if (blockIdx.y & 1) write_page<BF, true, BS, NU>(c, s, x, b, h, task, lds, red);
+  else write_page<BF, false, BS, NU>(c, s, x, b, h, task, lds, red);
 }
+
+// One page of one head back to 16 bits: keys and values [rows][H][D].
+template <bool BF, int BS, int NU>
+__global__ __launch_bounds__(BS) void cache_read_kernel(Cache c, Sequences s,
+                                                        uint16_t* __restrict__ k,
+                                                        uint16_t* __restrict__ v, int64_t rows) {
+  __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 32];
+  const int g = blockIdx.x, h = blockIdx.y >> 1, b = blockIdx.z, t = threadIdx.x;
+  const bool V = blockIdx.y & 1;
+  const int ps = c.ps, P = 1 << ps, D = c.D, D8 = D >> 3, p0 = g << ps;
+  // the sequence's rows are all of its tokens
+  const int64_t most = (int64_t)s.max_pages << ps;
+  const int len = (int)min((int64_t)max(s.lengths[b], 0), most);
+  if (p0 >= len) return;
+  const int64_t c0 = max((int64_t)s.cu[b], (int64_t)0) + p0;
+  const int n = (int)max(min((int64_t)min(P, len - p0), rows - c0), (int64_t)0);
+  uint16_t* out = (V ? v : k) + c0 * c.H * D + (int64_t)h * D;
+  const int64_t step = (int64_t)c.H * D;
+  if (p0 + P > len) {   // the tail, as it is
+    const int slot = s.slots ? s.slots[b] : b;
+    const bool ok = slot >= 0 && slot < c.n_slots;
+    const uint16_t* tail = (V ? c.vt : c.kt) + ((size_t)(ok ? slot : 0) * c.H + h) * P * D;
+    for (int q = t; q < n * D8; q += BS) {
+      const int p = q / D8, d8 = q % D8;
+      v4u r = {0, 0, 0, 0};
+      if (ok && !V) r = *reinterpret_cast<const v4u*>(tail + p * D + d8 * 8);
+      else if (ok)
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+          r[w >> 1] |= (uint32_t)tail[(d8 * 8 + w) * P + p] << (16 * (w & 1));
+      *reinterpret_cast<v4u*>(out + p * step + d8 * 8) = r;
+    }
+    return;
+  }
+  const int page = s.table[(size_t)b * s.max_pages + g];
+  const bool ok = page >= 0 && page < c.n_pages;   // (none: zeros)
+  const int8_t* in = (V ? c.vc : c.kc) + ((size_t)(ok ? page : 0) * c.H + h) * P * D;
+  const float scale = ok ? (V ? c.vs : c.ks)[(size_t)page * c.H + h] : 0.0f;
+  auto put = [&](int p, int d8, uint32_t lo, uint32_t hi) {   // 8 codes of one token
+    if (p >= n) return;
+    v4u r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = (i < 2 ? lo : hi) >> (16 * (i & 1));
+      const float f0 = ok ? (float)(int8_t)(uint8_t)x * scale : 0.0f;
+      const float f1 = ok ? (float)(int8_t)(uint8_t)(x >> 8) * scale : 0.0f;
+      r[i] = pack2<BF>(f0, f1);
+    }
+    *reinterpret_cast<v4u*>(out + p * step + d8 * 8) = r;
+  };
+  const int units = (P >> 2) * D8;
+  if (!V) {
+    uint2 w[NU][4];
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {   // 8 codes of a token each, the page in order
+        const int q = min(t + (4 * u + e) * BS, 4 * units - 1);
+        w[u][e] = *reinterpret_cast<const uint2*>(in + q * 8);
+      }
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int q = t + (4 * u + e) * BS;
+        if (q < 4 * units) put(q / D8, q % D8, w[u][e].x, w[u][e].y);
+      }
+    return;
+  }
+  v4u w[2 * NU];
+#pragma unroll
+  for (int u = 0; u < 2 * NU; ++u)
+    w[u] = *reinterpret_cast<const v4u*>(in + min(t + u * BS, 2 * units - 1) * 16);
+#pragma unroll
+  for (int u = 0; u < 2 * NU; ++u)
+    if (t + u * BS < 2 * units)
+      *reinterpret_cast<v4u*>(lds + page_piece(t + u * BS, ps) * 16) = w[u];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int q = t + u * BS, d8 = q % D8, t4 = q / D8 * 4;
+    if (q >= units) continue;
+    uint32_t k[2][4];   // [dimensions 0 .. 3, 4 .. 7][token]
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      uint32_t z[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t at = (uint32_t)(d8 * 8 + 4 * y + e) * P + t4;
+        z[e] = *reinterpret_cast<const uint32_t*>(lds + page_piece(at >> 4, ps) * 16 + (at & 15));
+      }
+      transpose4(z, k[y]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) put(t4 + e, d8, k[0][e], k[1][e]);
+  }
+}
+
+namespace {
+// Threads and units a thread for pages of P * D / 32 units.
+template <bool BF, int BS, int NU>
+void launch_write(const Cache& c, const Sequences& s, const CacheRows& x, dim3 grid,
+                  hipStream_t stream) {
+  hipLaunchKernelGGL((cache_write_kernel<BF, BS, NU>), grid, dim3(BS), 0, stream, c, s, x);
+}
+template <bool BF, int BS, int NU>
+void launch_read(const Cache& c, const Sequences& s, uint16_t* k, uint16_t* v, int64_t rows,
+                 dim3 grid, hipStream_t stream) {
+  hipLaunchKernelGGL((cache_read_kernel<BF, BS, NU>), grid, dim3(BS), 0, stream, c, s, k, v, rows);
+}
+#define I8L_CACHE_SIZES(F, ...)                                         \
+  do {                                                                  \
+    const int units = (c.D << c.ps) / 32;                               \
+    if (units <= 64) F(64, 1, __VA_ARGS__);                             \
+    else if (units <= 128) F(128, 1, __VA_ARGS__);                      \
+    else if (units <= 256) F(256, 1, __VA_ARGS__);                      \
+    else if (units <= 512) F(256, 2, __VA_ARGS__);                      \
+    else F(256, 4, __VA_ARGS__);                                        \
+  } while (0)
+}  // namespace
+
+static_assert(kMaxP * kMaxD / 32 <= 256 * 4, "the largest page");
 
 hipError_t launch_cache_write(const Cache& c, const Sequences& s, const uint16_t* k,
                               const uint16_t* v, int64_t k_ts, int64_t k_hs, int64_t v_ts,
@@ -165,81 +347,22 @@ hipError_t launch_cache_write(const Cache& c, const Sequences& s, const uint16_t
   const CacheRows x{{k, v}, {k_ts, v_ts}, {k_hs, v_hs}, rows};
   // max_new tokens touch at most this many pages (the first may hold others before them)
   const int tasks = (max_new + (1 << c.ps) - 2) / (1 << c.ps) + 1;
-  const dim3 grid(tasks, 2 * c.H, s.B), block(kCwThreads);
-  if (c.bf16) hipLaunchKernelGGL(cache_write_kernel<true>, grid, block, 0, stream, c, s, x);
-  else hipLaunchKernelGGL(cache_write_kernel<false>, grid, block, 0, stream, c, s, x);
+  const dim3 grid(tasks, 2 * c.H, s.B);
+#define I8L_W(BS, NU, BF) launch_write<BF, BS, NU>(c, s, x, grid, stream)
+  if (c.bf16) I8L_CACHE_SIZES(I8L_W, true);
+  else I8L_CACHE_SIZES(I8L_W, false);
+#undef I8L_W
   return hipGetLastError();
-}
-
-// One page of one head back to 16 bits: keys and values [rows][H][D].
-template <bool BF>
-__global__ __launch_bounds__(kCwThreads) void cache_read_kernel(Cache c, Sequences s,
-                                                                uint16_t* __restrict__ k,
-                                                                uint16_t* __restrict__ v,
-                                                                int64_t rows) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[kMaxP * kMaxD];
-  const int g = blockIdx.x, h = blockIdx.y >> 1, b = blockIdx.z, t = threadIdx.x;
-  const bool V = blockIdx.y & 1;
-  const int ps = c.ps, P = 1 << ps, D = c.D, D8 = D >> 3;
-  // the sequence's rows are all of its tokens
-  const int64_t most = (int64_t)s.max_pages << ps;
-  const int len = (int)min((int64_t)max(s.lengths[b], 0), most);
-  const int64_t c0 = max((int64_t)s.cu[b], (int64_t)0);
-  const int p0 = g << ps;
-  if (p0 >= len) return;
-  const int n = (int)min((int64_t)min(P, len - p0), rows - (c0 + p0));
-  const bool full = p0 + P <= len;
-  uint16_t* out = (V ? v : k) + (c0 + p0) * c.H * D + (int64_t)h * D;
-  const int64_t step = (int64_t)c.H * D;
-  float scale = 0.0f;
-  size_t base = 0;
-  bool ok;
-  if (full) {
-    const int page = s.table[(size_t)b * s.max_pages + g];
-    ok = page >= 0 && page < c.n_pages;
-    base = ((size_t)(ok ? page : 0) * c.H + h) * P * D;
-    if (ok) scale = (V ? c.vs : c.ks)[(size_t)page * c.H + h];
-  } else {
-    const int slot = s.slots ? s.slots[b] : b;
-    ok = slot >= 0 && slot < c.n_slots;
-    base = ((size_t)(ok ? slot : 0) * c.H + h) * P * D;
-  }
-  // 8 stored elements at q * 8 as 16-bit values
-  auto stored = [&](int q) -> v4u {
-    if (!ok) return v4u{0, 0, 0, 0};
-    if (!full) return *reinterpret_cast<const v4u*>((V ? c.vt : c.kt) + base + q * 8);
-    const uint2 w = *reinterpret_cast<const uint2*>((V ? c.vc : c.kc) + base + q * 8);
-    v4u r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t x = (i < 2 ? w.x : w.y) >> (16 * (i & 1));
-      r[i] = pack2<BF>((float)(int8_t)(uint8_t)x * scale, (float)(int8_t)(uint8_t)(x >> 8) * scale);
-    }
-    return r;
-  };
-  if (!V) {
-    for (int q = t; q < n * D8; q += kCwThreads)
-      *reinterpret_cast<v4u*>(out + (q / D8) * step + (q % D8) * 8) = stored(q);
-    return;
-  }
-  for (int q = t; q < P * D8; q += kCwThreads) {   // [D][P] in memory: transposed through LDS
-    const v4u r = stored(q);
-    const int d = q * 8 >> ps, p = q * 8 & (P - 1);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) lds[(p + e) * D + d] = (uint16_t)(r[e >> 1] >> (16 * (e & 1)));
-  }
-  __syncthreads();
-  for (int q = t; q < n * D8; q += kCwThreads)
-    *reinterpret_cast<v4u*>(out + (q / D8) * step + (q % D8) * 8) =
-        *reinterpret_cast<const v4u*>(lds + q * 8);
 }
 
 hipError_t launch_cache_read(const Cache& c, const Sequences& s, uint16_t* k, uint16_t* v,
                              int64_t rows, int max_len, hipStream_t stream) {
   const int pages = (max_len + (1 << c.ps) - 1) >> c.ps;
-  const dim3 grid(pages, 2 * c.H, s.B), block(kCwThreads);
-  if (c.bf16) hipLaunchKernelGGL(cache_read_kernel<true>, grid, block, 0, stream, c, s, k, v, rows);
-  else hipLaunchKernelGGL(cache_read_kernel<false>, grid, block, 0, stream, c, s, k, v, rows);
+  const dim3 grid(pages, 2 * c.H, s.B);
+#define I8L_R(BS, NU, BF) launch_read<BF, BS, NU>(c, s, k, v, rows, grid, stream)
+  if (c.bf16) I8L_CACHE_SIZES(I8L_R, true);
+  else I8L_CACHE_SIZES(I8L_R, false);
+#undef I8L_R
   return hipGetLastError();
 }
 
