@@ -214,8 +214,10 @@ template <bool BF, int BS, int NU>
 __global__ __launch_bounds__(BS) void cache_write_kernel(Cache c, Sequences s, CacheRows x) {
   __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 32];   // a page of values
   __shared__ uint32_t red[BS / 64];
-  const int task = blockIdx.x, h = blockIdx.y >> 1, b = blockIdx.z;
-  if (blockIdx.y & 1) write_page<BF, true, BS, NU>(c, s, x, b, h, task, lds, red);
+  // heads first: neighbours in a launch read neighbours in memory
+  const uint32_t hk = blockIdx.x % (2 * c.H);
+  const int task = blockIdx.x / (2 * c.H), h = hk >> 1, b = blockIdx.z;
+  if (hk & 1) write_page<BF, true, BS, NU>(c, s, x, b, h, task, lds, red);
   else write_page<BF, false, BS, NU>(c, s, x, b, h, task, lds, red);
 }
 
@@ -225,8 +227,9 @@ __global__ __launch_bounds__(BS) void cache_read_kernel(Cache c, Sequences s,
                                                         uint16_t* __restrict__ k,
                                                         uint16_t* __restrict__ v, int64_t rows) {
   __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 32];
-  const int g = blockIdx.x, h = blockIdx.y >> 1, b = blockIdx.z, t = threadIdx.x;
-  const bool V = blockIdx.y & 1;
+  const uint32_t hk = blockIdx.x % (2 * c.H);
+  const int g = blockIdx.x / (2 * c.H), h = hk >> 1, b = blockIdx.z, t = threadIdx.x;
+  const bool V = hk & 1;
   const int ps = c.ps, P = 1 << ps, D = c.D, D8 = D >> 3, p0 = g << ps;
   // the sequence's rows are all of its tokens
   const int64_t most = (int64_t)s.max_pages << ps;
@@ -347,7 +350,7 @@ hipError_t launch_cache_write(const Cache& c, const Sequences& s, const uint16_t
   const CacheRows x{{k, v}, {k_ts, v_ts}, {k_hs, v_hs}, rows};
   // max_new tokens touch at most this many pages (the first may hold others before them)
   const int tasks = (max_new + (1 << c.ps) - 2) / (1 << c.ps) + 1;
-  const dim3 grid(tasks, 2 * c.H, s.B);
+  const dim3 grid(tasks * 2 * c.H, 1, s.B);
 #define I8L_W(BS, NU, BF) launch_write<BF, BS, NU>(c, s, x, grid, stream)
   if (c.bf16) I8L_CACHE_SIZES(I8L_W, true);
   else I8L_CACHE_SIZES(I8L_W, false);
@@ -358,7 +361,7 @@ hipError_t launch_cache_write(const Cache& c, const Sequences& s, const uint16_t
 hipError_t launch_cache_read(const Cache& c, const Sequences& s, uint16_t* k, uint16_t* v,
                              int64_t rows, int max_len, hipStream_t stream) {
   const int pages = (max_len + (1 << c.ps) - 1) >> c.ps;
-  const dim3 grid(pages, 2 * c.H, s.B);
+  const dim3 grid(pages * 2 * c.H, 1, s.B);
 #define I8L_R(BS, NU, BF) launch_read<BF, BS, NU>(c, s, k, v, rows, grid, stream)
   if (c.bf16) I8L_CACHE_SIZES(I8L_R, true);
   else I8L_CACHE_SIZES(I8L_R, false);

@@ -6,6 +6,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "../../include/int8lin.h"
@@ -228,6 +229,14 @@ i8l_status check_count(const char* fn, const char* name, int64_t v, int64_t lo, 
   return I8L_OK;
 }
 
+// Workgroups of a launch: one for each page, head, and keys or values.
+i8l_status check_pages(const char* fn, const i8l::Cache& c, int64_t tokens) {
+  if (((tokens >> c.ps) + 2) * 2 * c.H > INT32_MAX)
+    return fail(I8L_ERR_INVALID_ARG, fn, "%lld tokens of %d heads are too many for one call",
+                (long long)tokens, c.H);
+  return I8L_OK;
+}
+
 constexpr int64_t kMaxRows = 1ll << 31;
 constexpr int64_t kMaxTokens = 1 << 30;
 
@@ -260,6 +269,9 @@ I8L_API i8l_status int8_cache_write(const i8l_kv_cache* cache, const i8l_sequenc
   CHECK(check_count(fn, "rows", rows, 0, kMaxRows));
   CHECK(check_count(fn, "max_new", max_new, 0, kMaxTokens));
   if (rows == 0 || max_new == 0 || s.B == 0 || s.max_pages == 0) return ok();
+  // no sequence gets more rows than the call has, nor more tokens than its pages hold
+  max_new = std::min(std::min(max_new, rows), (int64_t)s.max_pages << c.ps);
+  CHECK(check_pages(fn, c, max_new));
   CHECK(check_rows(fn, "k", k, k_token_stride, k_head_stride));
   CHECK(check_rows(fn, "v", v, v_token_stride, v_head_stride));
   (void)hipGetLastError();
@@ -279,6 +291,8 @@ I8L_API i8l_status int8_cache_read(const i8l_kv_cache* cache, const i8l_sequence
   CHECK(check_count(fn, "rows", rows, 0, kMaxRows));
   CHECK(check_count(fn, "max_len", max_len, 0, kMaxTokens));
   if (rows == 0 || max_len == 0 || s.B == 0 || s.max_pages == 0) return ok();
+  max_len = std::min(max_len, (int64_t)s.max_pages << c.ps);
+  CHECK(check_pages(fn, c, max_len));
   CHECK_PTR(k, 16);
   CHECK_PTR(v, 16);
   (void)hipGetLastError();
