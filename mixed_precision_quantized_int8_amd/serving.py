@@ -30,12 +30,24 @@ def _on(device):
         else torch.cuda.device(device)
 
 
+# the handle of torch's current stream (through the Stream object where this torch has
+# no direct way: 2 us of a call whose kernel takes 3)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
 def _dense(t, dtype, shape, device, name):
-    """A contiguous tensor of this type, shape and device (None: any)."""
+    """The pointer of a contiguous tensor of this type, shape and device (None: any
+    GPU); these calls are short, so what is right is settled first, what is wrong
+    said after."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.is_contiguous() and (t.is_cuda if device is None else t.device == device):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -44,9 +56,7 @@ def _dense(t, dtype, shape, device, name):
         raise ValueError(f"{name} must be on {device or 'a GPU'} (got {t.device})")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _half_type(t, name, dims):

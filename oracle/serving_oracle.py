@@ -87,33 +87,30 @@ def attention(q, k, v, scale, window=0, alibi=None, page_scale=None, u=2.0 ** -1
     G = Hq // H
     out = torch.zeros((m, Hq, D), dtype=F64)
     tol = torch.zeros_like(out)
-    t = torch.arange(n)
-    for i in range(m):
-        pos = n - m + i
-        seen = t <= pos
-        if window:
-            seen &= t > pos - window
-        seen = seen.nonzero()[:, 0]
-        if seen.numel() == 0:
-            continue
-        for h in range(Hq):
-            kk, vv = k[seen, h // G].to(F64), v[seen, h // G].to(F64)
-            qq = q[i, h].to(F64)
-            s = kk @ qq * scale
-            mag = kk.abs() @ qq.abs() * abs(scale)
-            if alibi is not None:
-                bias = float(alibi[h]) * (pos - seen).to(F64)
-                s = s - bias
-                mag = mag + bias.abs()
-            p = torch.softmax(s, 0)
-            o = p @ vv
-            es = (D + 8) * 2.0 ** -24 * float((mag + 64.0).max())
-            e = 2 * es + 2 * (seen.numel() + 64) * 2.0 ** -24
-            out[i, h] = o
-            tol[i, h] = (u + e) * (p @ vv.abs()) + u * o.abs() + 2.0 ** -24
-            if u < 2.0 ** -8:   # fp16: the weights' subnormal range
-                sv = torch.ones(seen.numel(), dtype=F64) if page_scale is None else \
-                    page_scale[seen, h // G].to(F64)
-                c = vv.abs() / torch.where(sv > 0, sv, torch.ones_like(sv))[:, None]
-                tol[i, h] += 2.0 ** -25 * (p * sv).max() * c.sum(0)
-    return out, tol
+    if n == 0:
+        return out, tol
+    back = torch.arange(n - m, n)[:, None] - torch.arange(n)[None]      # [m][n]
+    seen = back >= 0
+    if window:
+        seen &= back < window
+    count = seen.sum(1, keepdim=True).to(F64)
+    some = count[:, 0] > 0
+    for h in range(Hq):
+        kk, vv, qq = k[:, h // G].to(F64), v[:, h // G].to(F64), q[:, h].to(F64)
+        s = qq @ kk.T * scale
+        mag = qq.abs() @ kk.abs().T * abs(scale)
+        if alibi is not None:
+            bias = float(alibi[h]) * back.to(F64)
+            s, mag = s - bias, mag + bias.abs()
+        p = torch.softmax(s.masked_fill(~seen, -math.inf), dim=1)
+        p = torch.where(some[:, None], p, torch.zeros_like(p))
+        o = p @ vv
+        es = (D + 8) * 2.0 ** -24 * (torch.where(seen, mag, torch.zeros_like(mag)) + 64.0).amax(1, keepdim=True)
+        e = 2 * es + 2 * (count + 64) * 2.0 ** -24
+        out[:, h] = o
+        tol[:, h] = (u + e) * (p @ vv.abs()) + u * o.abs() + 2.0 ** -24
+        if u < 2.0 ** -8:   # fp16: the weights' subnormal range
+            sv = torch.ones(n, dtype=F64) if page_scale is None else page_scale[:, h // G].to(F64)
+            c = vv.abs() / torch.where(sv > 0, sv, torch.ones_like(sv))[:, None]
+            tol[:, h] += 2.0 ** -25 * (p * sv).amax(1, keepdim=True) * (seen.to(F64) @ c)
+    return out, torch.where(some[:, None, None], tol, torch.zeros_like(tol))

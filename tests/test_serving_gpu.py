@@ -399,6 +399,79 @@ def test_attention_runs_of_queries(lib, lens, Q, H, G, D, P, window, alibi, dtyp
     run_attention(w, G, Q, window, alibi)
 
 
+# sizes that take the kernel for runs of queries: 128 and 256 rows a workgroup, whole
+# and split, both padded head sizes, every page size, tails of one and two tiles
+WIDE_RUNS = [
+    # lens, queries, H, G, D, P, window, alibi
+    ([700, 333], [300, 290], 4, 4, 64, 16, 0, False),
+    ([700, 333], [300, 290], 4, 4, 128, 64, 0, True),
+    ([7000], [40], 8, 2, 128, 128, 0, False),           # 80 rows, split
+    ([5000, 100], [33, 100], 8, 2, 80, 32, 0, True),
+    ([2303], [129], 16, 1, 96, 128, 0, False),           # 129 rows: 256 a workgroup; tail 127
+    ([2800, 0, 2750], [260, 0, 150], 4, 3, 64, 64, 500, False),
+    ([2200], [256], 16, 4, 128, 16, 70, True),
+    ([1300, 1281], [513, 7], 8, 1, 128, 128, 1000, False),
+    ([4500], [2100], 2, 1, 112, 32, 0, False),
+    ([1025, 640, 511], [1025, 640, 400], 3, 2, 64, 128, 0, False),
+    ([2100], [2100], 32, 1, 64, 64, 0, False),           # 256 rows a workgroup, not split
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens,Q,H,G,D,P,window,alibi", WIDE_RUNS)
+def test_attention_wide_runs(lib, lens, Q, H, G, D, P, window, alibi, dtype):
+    say("attention, wide runs", lens, Q, H, G, D, P, window, alibi, dtype)
+    w = World(lib, lens, H, D, P, dtype, seed=sum(lens) + sum(Q))
+    run_attention(w, G, Q, window, alibi)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_wide_runs_extreme_values(lib, dtype):
+    """As test_attention_extreme_values, through the kernel for runs: maxima that rise
+    late and by much, value scales of many orders, pages of zeros."""
+    w = World(lib, [900, 700], 8, 64, 32, dtype, seed=18, fill=False)
+    w.v[0][:256] *= 2.0 ** -10
+    w.v[0][256:384] *= 512
+    w.v[0][512:576] = 0
+    w.k[0][576:640] = 0
+    w.k[0][640:] *= 20           # scores that leave the first ones far behind
+    w.k[1] *= 30
+    w.write([0, 0], w.lens)
+    run_attention(w, 2, [300, 300], q_scale=4.0)
+    run_attention(w, 2, [300, 700], window=90)
+
+
+def test_attention_wide_runs_hide_non_finite_pages(lib):
+    """A page of NaNs shows in the rows that see it and in no other, in both kernels'
+    masked tiles; a page number outside the cache hides its tokens."""
+    H, n, m = 8, 640, 400
+    w = World(lib, [n], H, 64, 16, "fp16", seed=19, fill=False)
+    clean = [x.clone() for x in (w.k[0], w.v[0])]
+    w.v[0][400, :, 1] = math.nan      # the page of tokens 400 .. 415
+    w.write([0], w.lens)
+    q = torch.randn((m, 2 * H, 64), generator=gen(2)).half()
+    y = lib.cache_attention(q.cuda(), w.cache, w.table, w.lengths, cu=w.cu([m]), slots=w.slots)
+    y = y.cpu().double()
+    first = 400 - (n - m)             # the first query that sees token 400 of the page
+    assert bool(y[first:].isnan().all())
+    st = O.Store(16)
+    k, (v, pages) = st.sequence(clean[0])[0], st.sequence(clean[1])
+    s = torch.ones((n, H))
+    for g, per in enumerate(pages):
+        for h in range(H):
+            s[g * 16:(g + 1) * 16, h] = per[h][1]
+    o, tol = O.attention(q[:first], k[:400], v[:400], 64 ** -0.5, page_scale=s[:400])
+    assert bool(((y[:first] - o).abs() <= tol).all())
+    # the page's number replaced: its tokens are out of sight, for all rows
+    table = w.table.clone()
+    table[0, 25] = -7
+    y = lib.cache_attention(q.cuda(), w.cache, table, w.lengths, cu=w.cu([m]), slots=w.slots)
+    keep = torch.cat([torch.arange(400), torch.arange(416, n)])
+    late = 416 - (n - m)
+    o, tol = O.attention(q[late:], k[keep], v[keep], 64 ** -0.5, page_scale=s[keep])
+    assert bool(((y[late:].cpu().double() - o).abs() <= tol).all())
+
+
 def test_attention_rows_that_see_nothing(lib):
     """More rows than tokens: the first queries come before the sequence's first
     token and give 0; so does every query of an empty sequence."""
