@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
   const int c0 = max(begin, lo_first & ~(kAdTile - 1)) + wave * kAdTile;
   const int c_end = min(end, coded);
   const int sub_k = 16 * (i16 >> 2), sub_v = 16 * grp;   // this lane's keys as K row, as P
-  const int8_t* k_at = a.c.kc + h * page_sz + (size_t)(((sub_k & (P - 1)) + (i16 & 3)) * D + 16 * grp);
+  const int8_t* k_at = a.c.kc + h * page_sz + (size_t)(((sub_k & (P - 1)) + (i16 & 3)) * D);
   const int8_t* v_at = a.c.vc + h * page_sz + (size_t)(i16 * P + (sub_v & (P - 1)));
   const uint32_t page_step = (uint32_t)(H * page_sz);   // at most 4096 * 128 * 256
   int pk = 0, pv = 0;          // pages of the tile to load next, as the table has them
@@ -212,15 +212,15 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
   };
   auto exists = [&](int page) { return (uint32_t)page < (uint32_t)a.c.n_pages; };
   auto load_k = [&](int t0) {
-    const int8_t* p = k_at + (uint64_t)(exists(pk) ? (uint32_t)pk : 0u) * page_step +
-                      (t0 & (P - 1) & kAdTile) * D;
+    const int8_t* at = k_at + (uint64_t)(exists(pk) ? (uint32_t)pk : 0u) * page_step +
+                       (t0 & (P - 1) & kAdTile) * D;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int c = 0; c < NC; ++c)   // an element past D meets a zero of q
-        if (D > 64 * c) {            // uniform
-          const int8_t* q = 64 * c + 16 * grp < D ? p + 64 * c : p;
-          kb[j][c] = *reinterpret_cast<const v4u*>(q + 4 * j * D);
+      for (int c = 0; c < NC; ++c)
+        if (64 * c < D) {   // uniform; a lane past D takes the row's start, which meets zeros of q
+          const int d = 64 * c + 16 * grp < D ? 64 * c + 16 * grp : 0;
+          kb[j][c] = *reinterpret_cast<const v4u*>(at + 4 * j * D + d);
         }
   };
   auto load_v = [&](int t0) {
@@ -385,9 +385,9 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
 constexpr int kApTile = 64;
 constexpr float kApSlack = 8.0f;
 
-template <bool BF, int DP, int NW, int RB, bool ALIBI>
-__global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(AttnArgs a) {
-  constexpr int NT = 64 * NW, kRows = 32 * NW * RB;
+template <bool BF, int DP, int NW, bool ALIBI>
+__global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
+  constexpr int NT = 64 * NW, kRows = 32 * NW;
   constexpr int NK = DP / 16;               // contraction steps of Q . K
   constexpr int ND = DP / 32;               // 32-row blocks of O^T
   constexpr int CH = 4 * DP;                // 16-code chunks of a tile of keys, and of values
@@ -415,28 +415,21 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
   if (r_wg >= n_rows) return;
   const int first_pos = sq.len - sq.n;      // position of query 0
 
-  // this lane's queries, one in each of the wave's RB blocks of 32 rows; rows past
-  // the end repeat the last
-  const int r_wave = r_wg + 32 * RB * wave;
-  int lo[RB], hi[RB], pos[RB], qi[RB], qg[RB];
-  bool live[RB];
-#pragma unroll
-  for (int w = 0; w < RB; ++w) {
-    const int r = r_wave + 32 * w + l32;
-    live[w] = r < n_rows;
-    qi[w] = min(r, n_rows - 1) / G;
-    qg[w] = min(r, n_rows - 1) % G;
-    pos[w] = first_pos + qi[w];
-    hi[w] = min(pos[w] + 1, sq.len);
-    lo[w] = a.window > 0 ? max(0, pos[w] + 1 - a.window) : 0;
-  }
+  // this lane's query; rows past the end repeat the last
+  const int r_wave = r_wg + 32 * wave;
+  const bool live = r_wave + l32 < n_rows;
+  const int rr = min(r_wave + l32, n_rows - 1);
+  const int qi = rr / G, qg = rr % G;
+  const int pos = first_pos + qi;
+  const int hi = min(pos + 1, sq.len);
+  const int lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
   auto low = [&](int row) -> int {   // first key that a row sees
     const int p = first_pos + row / G;
     return a.window > 0 ? max(0, p + 1 - a.window) : 0;
   };
   auto high = [&](int row) -> int { return min(first_pos + row / G + 1, sq.len); };
   // what every row of the wave sees, and what some row of the workgroup does
-  const int wv_lo1 = low(min(r_wave + 32 * RB, n_rows) - 1), wv_hi0 = high(min(r_wave, n_rows - 1));
+  const int wv_lo1 = low(min(r_wave + 32, n_rows) - 1), wv_hi0 = high(min(r_wave, n_rows - 1));
   const int wg_lo = low(r_wg), wg_hi = high(min(r_wg + kRows, n_rows) - 1);
 
   const int coded = sq.len >> ps << ps;
@@ -452,20 +445,15 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
   const int n_coded = c_end > c_begin ? (c_end - c_begin + kApTile - 1) / kApTile : 0;
   const int n_tail = end > coded && coded >= begin ? (end - coded + kApTile - 1) / kApTile : 0;
 
-  v4u qf[RB][NK];
-  float slope[RB];
+  v4u qf[NK];
 #pragma unroll
-  for (int w = 0; w < RB; ++w) {
-#pragma unroll
-    for (int s = 0; s < NK; ++s) {
-      const int d = 16 * s + 8 * hf;
-      qf[w][s] = v4u{0, 0, 0, 0};
-      if (live[w] && d < D)
-        qf[w][s] = *reinterpret_cast<const v4u*>(a.q + (sq.c0 + qi[w]) * a.q_ts +
-                                                 (h * G + qg[w]) * a.q_hs + d);
-    }
-    slope[w] = ALIBI ? a.alibi[h * G + qg[w]] * kLog2e : 0.0f;
+  for (int s = 0; s < NK; ++s) {
+    const int d = 16 * s + 8 * hf;
+    qf[s] = v4u{0, 0, 0, 0};
+    if (live && d < D)
+      qf[s] = *reinterpret_cast<const v4u*>(a.q + (sq.c0 + qi) * a.q_ts + (h * G + qg) * a.q_hs + d);
   }
+  const float slope = ALIBI ? a.alibi[h * G + qg] * kLog2e : 0.0f;
   const float sc = a.scale * kLog2e;
 
   // ---- staging -----------------------------------------------------------------
@@ -537,17 +525,14 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
 
   // ---- half a tile, 32 keys -------------------------------------------------------
   // maximum (0 until a key is seen: then limit is -inf) and sum (of this lane's keys)
-  float m[RB], limit[RB], l[RB];
-  v16f32 s[2][RB], o[RB][ND];
-  v4u p[RB][2];
+  float m, limit, l;
+  v16f32 s[2], o[ND];
+  v4u p[2];
+  m = l = 0.0f;
+  limit = -__builtin_inff();
+  p[0] = p[1] = v4u{0, 0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < RB; ++w) {
-    m[w] = l[w] = 0.0f;
-    limit[w] = -__builtin_inff();
-    p[w][0] = p[w][1] = v4u{0, 0, 0, 0};
-#pragma unroll
-    for (int d = 0; d < ND; ++d) o[w][d] = v16f32{};
-  }
+  for (int d = 0; d < ND; ++d) o[d] = v16f32{};
   const int row_k = (l32 & 0x13) | ((l32 & 4) << 1) | ((l32 & 8) >> 1);   // key of score row l32
   // LDS offsets of this lane's first fragments: the others differ in a constant and
   // in the piece's number, exchanged
@@ -561,76 +546,65 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
                                          (n % ND) * 32 * kApTile * 2);
   };
   v4f mul, base0, inv;   // of the tile at hand
-  float top[RB];
-  // Register 8 g + e of s[k]: key 32 k + 16 g + 8 hf + e.  Pair j of block w (two
+  float top;
+  // Register 8 g + e of s[k]: key 32 k + 16 g + 8 hf + e.  Pair j (two
   // neighbours): scores less the maximum so far, and the highest of them;
-  float bias[RB][2];
-  auto bias_of = [&](int t0, int k, int w, int g) {
-    const float x = base0[2 * k + g] - m[w];
-    return ALIBI ? __builtin_fmaf(slope[w], (float)(t0 + 32 * k + 16 * g + 8 * hf - pos[w]), x) : x;
+  float bias[2];
+  auto bias_of = [&](int t0, int k, int g) {
+    const float x = base0[2 * k + g] - m;
+    return ALIBI ? __builtin_fmaf(slope, (float)(t0 + 32 * k + 16 * g + 8 * hf - pos), x) : x;
   };
-  auto shift = [&](int k, int w, int j) {
+  auto shift = [&](int k, int j) {
 #pragma unroll
     for (int e = 2 * j; e < 2 * j + 2; ++e) {
-      float x = __builtin_fmaf(s[k][w][e], mul[2 * k + (e >> 3)], bias[w][e >> 3]);
-      if (ALIBI) x = __builtin_fmaf(slope[w], (float)(e & 7), x);
-      s[k][w][e] = x;
-      top[w] = __builtin_fmaxf(top[w], x);
+      float x = __builtin_fmaf(s[k][e], mul[2 * k + (e >> 3)], bias[e >> 3]);
+      if (ALIBI) x = __builtin_fmaf(slope, (float)(e & 7), x);
+      s[k][e] = x;
+      top = __builtin_fmaxf(top, x);
     }
   };
   // scores to weights in 16 bits, and their sum.
-  float add[RB][2];
-  auto weigh = [&](int k, int w, int j) {
-    const float w0 = __builtin_amdgcn_exp2f(s[k][w][2 * j]);
-    const float w1 = __builtin_amdgcn_exp2f(s[k][w][2 * j + 1]);
+  float add[2];
+  auto weigh = [&](int k, int j) {
+    const float w0 = __builtin_amdgcn_exp2f(s[k][2 * j]);
+    const float w1 = __builtin_amdgcn_exp2f(s[k][2 * j + 1]);
     uint32_t pair = pack2<BF>(w0, w1);
     asm volatile("" : "+v"(pair));   // formed in its slot, not next to its use
-    p[w][j >> 2][j & 3] = pair;
-    add[w][j >> 2] += w0 + w1;
+    p[j >> 2][j & 3] = pair;
+    add[j >> 2] += w0 + w1;
   };
   auto total = [&](int k) {
 #pragma unroll
-    for (int w = 0; w < RB; ++w)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) l[w] = __builtin_fmaf(add[w][g], inv[2 * k + g], l[w]);
+    for (int g = 0; g < 2; ++g) l = __builtin_fmaf(add[g], inv[2 * k + g], l);
   };
   // masks the scores where a row of the wave does not see a key; moves the maximum
   auto settle = [&](int tile0, int k) {
     const int t0 = tile0 + 32 * k;
     if (!(t0 >= wv_lo1 && t0 + 32 <= wv_hi0)) {   // uniform
+      top = -__builtin_inff();
 #pragma unroll
-      for (int w = 0; w < RB; ++w) {
-        top[w] = -__builtin_inff();
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = t0 + 16 * (r >> 3) + 8 * hf + (r & 7);
-          const float x = key >= lo[w] && key < hi[w] ? s[k][w][r] : -__builtin_inff();
-          s[k][w][r] = x;
-          top[w] = __builtin_fmaxf(top[w], x);
-        }
+      for (int r = 0; r < 16; ++r) {
+        const int key = t0 + 16 * (r >> 3) + 8 * hf + (r & 7);
+        const float x = key >= lo && key < hi ? s[k][r] : -__builtin_inff();
+        s[k][r] = x;
+        top = __builtin_fmaxf(top, x);
       }
     }
-    bool move = false;
+    if (__any(top > limit)) {
+      float a0, a1;   // both halves of the wave hold the same queries
+      halves(top, &a0, &a1);
+      const float high = __builtin_fmaxf(a0, a1);
+      const bool fresh = limit < 0.0f, some = high > -__builtin_inff();
+      // the maximum moves by `up` (at first from nothing, to the tile's)
+      const float up = some ? (fresh ? high : __builtin_fmaxf(high, 0.0f)) : 0.0f;
+      const float f = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up);
+      m += up;
+      if (some) limit = kApSlack;
+      l *= f;
 #pragma unroll
-    for (int w = 0; w < RB; ++w) move |= top[w] > limit[w];
-    if (__any(move)) {
+      for (int d = 0; d < ND; ++d) o[d] *= f;
 #pragma unroll
-      for (int w = 0; w < RB; ++w) {
-        float a0, a1;   // both halves of the wave hold the same queries
-        halves(top[w], &a0, &a1);
-        const float high = __builtin_fmaxf(a0, a1);
-        const bool fresh = limit[w] < 0.0f, some = high > -__builtin_inff();
-        // the maximum moves by `up` (at first from nothing, to the tile's)
-        const float up = some ? (fresh ? high : __builtin_fmaxf(high, 0.0f)) : 0.0f;
-        const float f = fresh ? 1.0f : __builtin_amdgcn_exp2f(-up);
-        m[w] += up;
-        if (some) limit[w] = kApSlack;
-        l[w] *= f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[w][d] *= f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[k][w][r] -= up;
-      }
+      for (int r = 0; r < 16; ++r) s[k][r] -= up;
     }
   };
   // Half k of tile i.  A wave issues in order, so the matrix cores and the vector
@@ -649,40 +623,28 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
     v4u f[kAhead];
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) f[n] = fragment(n);
+    top = -__builtin_inff();
 #pragma unroll
-    for (int w = 0; w < RB; ++w) {
-      top[w] = -__builtin_inff();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) bias[w][g] = bias_of(t0, k, w, g);
-    }
+    for (int g = 0; g < 2; ++g) bias[g] = bias_of(t0, k, g);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
+      __builtin_amdgcn_sched_barrier(0);
+      o[n % ND] = mfma32<BF>(f[n % kAhead], p[n / ND], o[n % ND]);
 #pragma unroll
-      for (int w = 0; w < RB; ++w) {
-        __builtin_amdgcn_sched_barrier(0);
-        o[w][n % ND] = mfma32<BF>(f[n % kAhead], p[w][n / ND], o[w][n % ND]);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) shift(k, w, n * kPairs + j);
-      }
+      for (int j = 0; j < kPairs; ++j) shift(k, n * kPairs + j);
       f[n % kAhead] = fragment(n + kAhead);
       extra(n);
     }
     __builtin_amdgcn_sched_barrier(0);
     settle(t0, k);
-#pragma unroll
-    for (int w = 0; w < RB; ++w) {
-      add[w][0] = add[w][1] = 0.0f;
-      s[k ^ 1][w] = v16f32{};
-    }
+    add[0] = add[1] = 0.0f;
+    s[k ^ 1] = v16f32{};
 #pragma unroll
     for (int n = NV; n < NV + NK; ++n) {
+      __builtin_amdgcn_sched_barrier(0);
+      s[k ^ 1] = mfma32<BF>(f[n % kAhead], qf[n - NV], s[k ^ 1]);
 #pragma unroll
-      for (int w = 0; w < RB; ++w) {
-        __builtin_amdgcn_sched_barrier(0);
-        s[k ^ 1][w] = mfma32<BF>(f[n % kAhead], qf[w][n - NV], s[k ^ 1][w]);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) weigh(k, w, (n - NV) * kPairs + j);
-      }
+      for (int j = 0; j < kPairs; ++j) weigh(k, (n - NV) * kPairs + j);
       if (n + kAhead < NV + NK) f[n % kAhead] = fragment(n + kAhead);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -696,23 +658,14 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
   };
   auto first_scores = [&](int i, int k) {
     const uint32_t at = at_k + (uint32_t)(i & 1) * kBuf;
+    s[k] = v16f32{};
 #pragma unroll
-    for (int w = 0; w < RB; ++w) s[k][w] = v16f32{};
-#pragma unroll
-    for (int u = 0; u < NK; ++u) {
-      const v4u f = frag_k(at, u, k);
-#pragma unroll
-      for (int w = 0; w < RB; ++w) s[k][w] = mfma32<BF>(f, qf[w][u], s[k][w]);
-    }
+    for (int u = 0; u < NK; ++u) s[k] = mfma32<BF>(frag_k(at, u, k), qf[u], s[k]);
   };
   auto last_outputs = [&](int i, int k) {
     const uint32_t at = at_v + (uint32_t)(i & 1) * kBuf;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const v4u f = frag_v(at, n, k);
-#pragma unroll
-      for (int w = 0; w < RB; ++w) o[w][n % ND] = mfma32<BF>(f, p[w][n / ND], o[w][n % ND]);
-    }
+    for (int n = 0; n < NV; ++n) o[n % ND] = mfma32<BF>(frag_v(at, n, k), p[n / ND], o[n % ND]);
   };
 
   // ---- the loop over complete pages ----------------------------------------------
@@ -804,62 +757,54 @@ __global__ __launch_bounds__(64 * NW, RB == 2 ? 1 : 2) void attn_run_kernel(Attn
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       first_scores(0, k);
+      top = -__builtin_inff();
+      add[0] = add[1] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < RB; ++w) {
-        top[w] = -__builtin_inff();
-        add[w][0] = add[w][1] = 0.0f;
+      for (int g = 0; g < 2; ++g) bias[g] = bias_of(t0, k, g);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) bias[w][g] = bias_of(t0, k, w, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) shift(k, w, e);
-      }
+      for (int e = 0; e < 8; ++e) shift(k, e);
       settle(t0, k);
 #pragma unroll
-      for (int w = 0; w < RB; ++w)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) weigh(k, w, e);
+      for (int e = 0; e < 8; ++e) weigh(k, e);
       total(k);
       last_outputs(0, k);
     }
   }
 
-#pragma unroll
-  for (int w = 0; w < RB; ++w) {
-    float l_lo, l_hi;
-    halves(l[w], &l_lo, &l_hi);
-    const float sum = l_lo + l_hi;
-    if (!live[w]) continue;
-    if (a.n_split == 1) {
-      const int64_t row_out = (sq.c0 + qi[w]) * H * G + h * G + qg[w];
-      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key at all: 0
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int at = 32 * d + 8 * q + 4 * hf;
-          if (at < D) {
-            uint2 x;
-            x.x = pack2<BF>(o[w][d][4 * q] * f, o[w][d][4 * q + 1] * f);
-            x.y = pack2<BF>(o[w][d][4 * q + 2] * f, o[w][d][4 * q + 3] * f);
-            *reinterpret_cast<uint2*>(a.out + row_out * D + at) = x;
-          }
-        }
-      continue;
-    }
-    const size_t at = part_at(a, b, h, r_wave + 32 * w + l32, split);
+  float l_lo, l_hi;
+  halves(l, &l_lo, &l_hi);
+  const float sum = l_lo + l_hi;
+  if (!live) return;
+  if (a.n_split == 1) {
+    const int64_t row_out = (sq.c0 + qi) * H * G + h * G + qg;
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key at all: 0
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int e = 32 * d + 8 * q + 4 * hf;
-        if (e < D)
-          *reinterpret_cast<v4f*>(part_out(a, at) + e) =
-              v4f{o[w][d][4 * q], o[w][d][4 * q + 1], o[w][d][4 * q + 2], o[w][d][4 * q + 3]};
+        const int at = 32 * d + 8 * q + 4 * hf;
+        if (at < D) {
+          uint2 x;
+          x.x = pack2<BF>(o[d][4 * q] * f, o[d][4 * q + 1] * f);
+          x.y = pack2<BF>(o[d][4 * q + 2] * f, o[d][4 * q + 3] * f);
+          *reinterpret_cast<uint2*>(a.out + row_out * D + at) = x;
+        }
       }
-    if (hf == 0) {
-      a.part[2 * at] = limit[w] < 0.0f ? -__builtin_inff() : m[w];
-      a.part[2 * at + 1] = sum;
+    return;
+  }
+  const size_t at = part_at(a, b, h, rr, split);
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int e = 32 * d + 8 * q + 4 * hf;
+      if (e < D)
+        *reinterpret_cast<v4f*>(part_out(a, at) + e) =
+            v4f{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
     }
+  if (hf == 0) {
+    a.part[2 * at] = limit < 0.0f ? -__builtin_inff() : m;
+    a.part[2 * at + 1] = sum;
   }
 }
 
@@ -923,27 +868,38 @@ struct Plan {
 };
 Plan plan(int B, int H, int G, int D, int max_q, int max_len, int window) {
   Plan p;
-  int range = max_len;
-  if (window > 0) range = (int)std::min((int64_t)max_len, (int64_t)window + max_q + 128);
   const int64_t rows = (int64_t)G * max_q, heads = (int64_t)B * H;
+  // keys that a tile of `n` rows sees (from a multiple of 128 on)
+  auto range_of = [&](int n) -> int64_t {
+    return window > 0 ? std::min((int64_t)max_len, (int64_t)window + n / G + 129) : max_len;
+  };
   // Up to 16 rows are one tile of attn_decode_kernel, which reads the keys once for
-  // each 16 rows; more take attn_run_kernel, unless the whole call is so short that
-  // its longer way per tile shows (8 kv heads, 1024 keys: 128 rows 12.7 against
-  // 18.4 us, 256 rows 16.9 against 20.2, 512 rows 25.6 against 22.5).
+  // each 16 rows; more take attn_run_kernel, unless the call is so short that its
+  // longer way per tile, or the join of a split, shows (8 kv heads: 256 rows over 1024
+  // keys 16.6 against 20.0 us, 2048 rows 32.2 against 39.3; 64 rows over 8192 keys 27.8
+  // against 24.2, 256 rows 69 against 37), or it has so few rows more over so many
+  // keys that it does not keep memory as busy (64 heads, 32 rows over 65536 keys: 296
+  // against 382; 64 rows 487 against 375).
   p.rows = 16;
-  if (rows > 16 && D <= 128 && heads * ((rows + 15) / 16) * range > (1 << 18)) {
+  const int64_t keys = heads * range_of(16);
+  if (rows > 16 && D <= 128 &&
+      keys * ((rows + 15) / 16) > (range_of(16) <= 1024 ? 1 << 20 : 1 << 18) &&
+      !(rows <= 32 && keys >= (1 << 22))) {
     // Wider tiles stage and convert a key for more rows (8 kv heads, 2048 rows over
     // 8192 keys: 128 -> 93 us); narrow ones where the rows, or a short range, would
     // leave compute units idle (64 heads, 512 rows over 1024 keys: 54 -> 37 us).
     const int64_t wide = heads * ((rows + 255) / 256);
-    p.rows = rows > 128 && (wide >= 256 || range > 2048) ? 256 : 128;
+    p.rows = rows > 128 && (wide >= 256 || range_of(256) > 2048) ? 256 : 128;
   }
-  // Splits of at least 256 keys, for about 16 (single rows: ragged lengths even out),
-  // 2 or 1 workgroups a compute unit.
+  // Splits for about 16 (single rows: ragged lengths even out), 2 or 1 workgroups a
+  // compute unit; of at least 256 keys, or 1024 where the tiles alone fill the chip
+  // (the join is a launch more).
+  const int64_t range = range_of(p.rows);
   const int64_t tiles = heads * ((rows + p.rows - 1) / p.rows);
   const int64_t fill = p.rows == 16 ? 4096 : p.rows == 128 ? 512 : 256;
   const int64_t want = std::max<int64_t>(fill / tiles, 1);
-  const int64_t c = std::max<int64_t>(((range + want - 1) / want + 255) / 256 * 256, 256);
+  const int64_t c = std::max<int64_t>(((range + want - 1) / want + 255) / 256 * 256,
+                                      tiles >= 256 ? 1024 : 256);
   p.chunk = (int)c;
   p.n_split = std::max((int)((range + c - 1) / c), 1);
   return p;
@@ -961,12 +917,12 @@ void launch_kernel(const AttnArgs& a, const Plan& p, hipStream_t stream) {
     else hipLaunchKernelGGL((attn_decode_kernel<BF, 256, ALIBI>), grid, block, 0, stream, a);
   } else if (p.rows == 128) {
     if (D <= 64)
-      hipLaunchKernelGGL((attn_run_kernel<BF, 64, 4, 1, ALIBI>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 4, 1, ALIBI>), grid, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((attn_run_kernel<BF, 64, 4, ALIBI>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 4, ALIBI>), grid, dim3(256), 0, stream, a);
   } else {
     if (D <= 64)
-      hipLaunchKernelGGL((attn_run_kernel<BF, 64, 8, 1, ALIBI>), grid, dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 8, 1, ALIBI>), grid, dim3(512), 0, stream, a);
+      hipLaunchKernelGGL((attn_run_kernel<BF, 64, 8, ALIBI>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 8, ALIBI>), grid, dim3(512), 0, stream, a);
   }
 }
 

@@ -366,6 +366,9 @@ SINGLE = [
     ([1500, 900], 1, 20, 64, 64, 0, False),
     ([5000], 1, 2, 128, 64, 0, True),
     ([3000], 2, 2, 96, 128, 1000, False),
+    ([100, 64], 2, 2, 16, 16, 0, False),
+    ([300], 1, 3, 32, 32, 0, True),
+    ([257, 130], 2, 1, 48, 128, 0, False),
 ]
 
 
@@ -403,17 +406,19 @@ def test_attention_runs_of_queries(lib, lens, Q, H, G, D, P, window, alibi, dtyp
 # and split, both padded head sizes, every page size, tails of one and two tiles
 WIDE_RUNS = [
     # lens, queries, H, G, D, P, window, alibi
-    ([700, 333], [300, 290], 4, 4, 64, 16, 0, False),
-    ([700, 333], [300, 290], 4, 4, 128, 64, 0, True),
+    ([1100, 333], [300, 290], 4, 4, 64, 16, 0, False),
+    ([1100, 333], [300, 290], 4, 4, 128, 64, 0, True),
     ([7000], [40], 8, 2, 128, 128, 0, False),           # 80 rows, split
     ([5000, 100], [33, 100], 8, 2, 80, 32, 0, True),
     ([2303], [129], 16, 1, 96, 128, 0, False),           # 129 rows: 256 a workgroup; tail 127
-    ([2800, 0, 2750], [260, 0, 150], 4, 3, 64, 64, 500, False),
-    ([2200], [256], 16, 4, 128, 16, 70, True),
+    ([2800, 0, 2750], [520, 0, 300], 8, 3, 64, 64, 500, False),
+    ([1100], [512], 48, 4, 64, 16, 70, True),
     ([1300, 1281], [513, 7], 8, 1, 128, 128, 1000, False),
     ([4500], [2100], 2, 1, 112, 32, 0, False),
     ([1025, 640, 511], [1025, 640, 400], 3, 2, 64, 128, 0, False),
     ([2100], [2100], 32, 1, 64, 64, 0, False),           # 256 rows a workgroup, not split
+    ([1100, 1040], [400, 333], 6, 3, 16, 16, 0, False),
+    ([1100, 1040], [400, 333], 6, 3, 48, 64, 0, True),
 ]
 
 
@@ -429,7 +434,7 @@ def test_attention_wide_runs(lib, lens, Q, H, G, D, P, window, alibi, dtype):
 def test_attention_wide_runs_extreme_values(lib, dtype):
     """As test_attention_extreme_values, through the kernel for runs: maxima that rise
     late and by much, value scales of many orders, pages of zeros."""
-    w = World(lib, [900, 700], 8, 64, 32, dtype, seed=18, fill=False)
+    w = World(lib, [1200, 700], 8, 64, 32, dtype, seed=18, fill=False)
     w.v[0][:256] *= 2.0 ** -10
     w.v[0][256:384] *= 512
     w.v[0][512:576] = 0
@@ -438,13 +443,13 @@ def test_attention_wide_runs_extreme_values(lib, dtype):
     w.k[1] *= 30
     w.write([0, 0], w.lens)
     run_attention(w, 2, [300, 300], q_scale=4.0)
-    run_attention(w, 2, [300, 700], window=90)
+    run_attention(w, 2, [300, 700], window=900)
 
 
 def test_attention_wide_runs_hide_non_finite_pages(lib):
     """A page of NaNs shows in the rows that see it and in no other, in both kernels'
     masked tiles; a page number outside the cache hides its tokens."""
-    H, n, m = 8, 640, 400
+    H, n, m = 8, 1280, 1000
     w = World(lib, [n], H, 64, 16, "fp16", seed=19, fill=False)
     clean = [x.clone() for x in (w.k[0], w.v[0])]
     w.v[0][400, :, 1] = math.nan      # the page of tokens 400 .. 415
