@@ -32,6 +32,7 @@ constexpr float kLeastScale = 0x1p-100f;
 struct Rows {          // a sequence's part of the call
   int64_t c0;          // first row in q and out
   int n, len;          // queries, tokens held
+  int first_pos;       // position of its first query
 };
 __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int b) {
   Rows r;
@@ -41,7 +42,8 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int b) {
   c0 = min(max(c0, (int64_t)0), a.rows);
   c1 = min(max(c1, c0), a.rows);
   r.c0 = c0;
-  r.n = (int)min(c1 - c0, (int64_t)a.max_q);
+  r.n = (int)min(c1 - c0, (int64_t)a.max_q);   // (none past max_q is written)
+  r.first_pos = (int)max((int64_t)r.len - (c1 - c0), -((int64_t)1 << 30));
   return r;
 }
 
@@ -97,15 +99,15 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
   const bool live = r < n_rows;
   const int rr = live ? r : n_rows - 1;
   const int qi = rr / G, qg = rr % G;
-  const int pos = sq.len - sq.n + qi;              // its position; keys <= pos
+  const int pos = sq.first_pos + qi;              // its position; keys <= pos
   const int hi = min(pos + 1, sq.len);
   const int lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
   // the tile's range (rows are in the order of their positions)
   const int q_last = (min(r0 + 16, n_rows) - 1) / G;
-  const int all_hi = min(sq.len - sq.n + q_last + 1, sq.len);
-  const int lo_first = a.window > 0 ? max(0, sq.len - sq.n + r0 / G + 1 - a.window) : 0;
-  const int hi_first = min(sq.len - sq.n + r0 / G + 1, sq.len);       // seen by every row
-  const int lo_last = a.window > 0 ? max(0, sq.len - sq.n + q_last + 1 - a.window) : 0;
+  const int all_hi = min(sq.first_pos + q_last + 1, sq.len);
+  const int lo_first = a.window > 0 ? max(0, sq.first_pos + r0 / G + 1 - a.window) : 0;
+  const int hi_first = min(sq.first_pos + r0 / G + 1, sq.len);       // seen by every row
+  const int lo_last = a.window > 0 ? max(0, sq.first_pos + q_last + 1 - a.window) : 0;
   // keys of this split: whole pages of any size (128 divides begin and chunk)
   const int first = lo_first & ~127;
   const int begin = first + split * a.chunk;
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
   const int tiles = (int)gridDim.x / H;
   const int r_wg = (tiles - 1 - (int)blockIdx.x / H) * kRows;
   if (r_wg >= n_rows) return;
-  const int first_pos = sq.len - sq.n;      // position of query 0
+  const int first_pos = sq.first_pos;
 
   // this lane's query; rows past the end repeat the last
   const int r_wave = r_wg + 32 * wave;

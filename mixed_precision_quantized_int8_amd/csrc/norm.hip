@@ -21,9 +21,8 @@ constexpr int kNormChunk = 8;   // elements per 16-byte load
 // its row, chunk t + i * TPR.  K % 16 == 0, K <= TPR * NCH * 8.
 template <int BS, int TPR, int NCH, bool BF>
 __global__ __launch_bounds__(BS) void rmsnorm_quant_kernel(
-    const uint16_t* __restrict__ X, const uint16_t* __restrict__ R, const uint16_t* __restrict__ W,
-    int M, int K, float eps, int8_t* __restrict__ Xq, float* __restrict__ sx,
-    uint16_t* __restrict__ H) {
+    const uint16_t* X, const uint16_t* R, const uint16_t* __restrict__ W, int M, int K, float eps,
+    int8_t* __restrict__ Xq, float* __restrict__ sx, uint16_t* H) {   // H may be X or R
   constexpr int RPB = BS / TPR;
   const int t = threadIdx.x % TPR;
   const int row = blockIdx.x * RPB + threadIdx.x / TPR;

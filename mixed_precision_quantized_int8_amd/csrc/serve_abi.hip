@@ -153,7 +153,8 @@ I8L_API i8l_status int8_linear_codes(const int8_t* Xq, const float* sx, int64_t 
                   p.workspace);
   }
   const int32_t* zeros = nullptr;
-  CHECK(zero_words(fn, &zeros));
+  if (p.kind != i8l::CodesPlan::kRows && p.kind != i8l::CodesPlan::kTiles)
+    CHECK(zero_words(fn, &zeros));   // the layer's own kernels read an outlier count
   (void)hipGetLastError();
   const i8l::CodesArgs a{Xq, sx, Wq, sw, bias, Y,
                          p.workspace ? static_cast<int32_t*>(workspace) : nullptr,
@@ -309,6 +310,7 @@ I8L_API size_t i8l_attention_workspace_bytes(const i8l_kv_cache* cache, int64_t 
       check_attention(fn, c, q_heads, max_q, max_len, window) != I8L_OK)
     return 0;
   if (n == 0) return 0;
+  window = std::min(window, kMaxTokens);
   return sizeof(float) * i8l::attention_partials((int)n, c.H, (int)(q_heads / c.H), c.D,
                                                  (int)max_q, (int)max_len, (int)window);
 }
@@ -333,6 +335,7 @@ I8L_API i8l_status int8_cache_attention(const i8l_kv_cache* cache, const i8l_seq
   CHECK(check_rows(fn, "q", q, q_token_stride, q_head_stride));
   CHECK_PTR(out, 16);
   if (alibi) CHECK_PTR(alibi, 4);
+  window = std::min(window, kMaxTokens);   // (no position is as far; sums of the two stay in 32 bits)
   const size_t need = sizeof(float) * i8l::attention_partials(s.B, c.H, (int)(q_heads / c.H), c.D,
                                                               (int)max_q, (int)max_len,
                                                               (int)window);

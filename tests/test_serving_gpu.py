@@ -108,6 +108,8 @@ def test_rmsnorm_quant_non_finite_rows(lib):
 CODES = [(1, 16, 1), (1, 4096, 1000), (8, 4096, 16384), (16, 1024, 33), (17, 272, 130), (64, 2064, 1300),
          (65, 528, 257), (128, 1040, 64), (129, 1024, 300), (256, 4096, 515), (257, 80, 300), (520, 2048, 1300),
          (700, 1040, 77)]
+# the layer's own kernels on codes: streaming, skinny tiles, 256 x 256 tiles whole and split
+CODES += [(32, 1040, 5000), (3, 528, 8500), (80, 272, 16400), (200, 1040, 16500), (300, 80, 16640), (512, 2048, 33000)]
 
 
 @pytest.mark.parametrize("M,K,N", CODES)
@@ -540,6 +542,20 @@ def test_attention_strided_queries_and_hints(lib):
         for b, (k, v, s) in enumerate(w.stored()):
             o, tol = O.attention(q[b:b + 1], k, v, 64 ** -0.5, page_scale=s)
             assert bool(((y[b:b + 1].cpu().double() - o).abs() <= tol).all()), max_len
+
+
+def test_attention_rows_past_max_q_are_not_written(lib):
+    """max_q below a sequence's rows: the first rows are right, the others untouched;
+    a window past any position is none."""
+    w = World(lib, [90, 33], 1, 64, 16, "fp16", seed=21)
+    q = torch.randn((12, 2, 64), generator=gen(5)).half().cuda()
+    args = (q, w.cache, w.table, w.lengths)
+    whole = lib.cache_attention(*args, cu=w.cu([7, 5]), slots=w.slots, window=2 ** 31 - 1)
+    out = torch.full_like(q, 7.0)
+    lib.cache_attention(*args, cu=w.cu([7, 5]), slots=w.slots, max_q=6, out=out)
+    same(out[:6], whole[:6])
+    same(out[7:], whole[7:])
+    assert bool((out[6] == 7.0).all())
 
 
 def test_attention_is_deterministic_on_any_stream(lib):
