@@ -388,7 +388,7 @@ constexpr int kApTile = 64;
 constexpr float kApSlack = 8.0f;
 
 template <bool BF, int DP, int NW, bool ALIBI>
-__global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(AttnArgs a) {
   constexpr int NT = 64 * NW, kRows = 32 * NW;
   constexpr int NK = DP / 16;               // contraction steps of Q . K
   constexpr int ND = DP / 32;               // 32-row blocks of O^T
@@ -615,7 +615,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
   // products of the next half tile's scores with this one's weights, in slots of
   // one product and its share of the vector work.  Fragments are read kAhead steps
   // before their use; `extra(n)` is more vector work for the first NV slots.
-  constexpr int kAhead = 4, NV = 2 * ND, kPairs = 8 / NK;   // pairs of a block per slot
+  constexpr int kAhead = 4, NV = 2 * ND;   // (8 pairs over NV, then over NK slots)
   auto half_tile = [&](int i, int k, auto extra) {
     const int t0 = c_begin + i * kApTile;
     uint32_t av = at_v + (uint32_t)((k ? i : i - 1) & 1) * kBuf;
@@ -633,7 +633,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
       __builtin_amdgcn_sched_barrier(0);
       o[n % ND] = mfma32<BF>(f[n % kAhead], p[n / ND], o[n % ND]);
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) shift(k, n * kPairs + j);
+      for (int j = n * 8 / NV; j < (n + 1) * 8 / NV; ++j) shift(k, j);
       f[n % kAhead] = fragment(n + kAhead);
       extra(n);
     }
@@ -646,7 +646,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_run_kernel(AttnArgs a) {
       __builtin_amdgcn_sched_barrier(0);
       s[k ^ 1] = mfma32<BF>(f[n % kAhead], qf[n - NV], s[k ^ 1]);
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) weigh(k, (n - NV) * kPairs + j);
+      for (int j = (n - NV) * 8 / NK; j < (n - NV + 1) * 8 / NK; ++j) weigh(k, j);
       if (n + kAhead < NV + NK) f[n % kAhead] = fragment(n + kAhead);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -884,14 +884,14 @@ Plan plan(int B, int H, int G, int D, int max_q, int max_len, int window) {
   // against 382; 64 rows 487 against 375).
   p.rows = 16;
   const int64_t keys = heads * range_of(16);
-  if (rows > 16 && D <= 128 &&
+  if (rows > 16 &&
       keys * ((rows + 15) / 16) > (range_of(16) <= 1024 ? 1 << 20 : 1 << 18) &&
       !(rows <= 32 && keys >= (1 << 22))) {
     // Wider tiles stage and convert a key for more rows (8 kv heads, 2048 rows over
     // 8192 keys: 128 -> 93 us); narrow ones where the rows, or a short range, would
     // leave compute units idle (64 heads, 512 rows over 1024 keys: 54 -> 37 us).
     const int64_t wide = heads * ((rows + 255) / 256);
-    p.rows = rows > 128 && (wide >= 256 || range_of(256) > 2048) ? 256 : 128;
+    p.rows = rows > 128 && D <= 128 && (wide >= 256 || range_of(256) > 2048) ? 256 : 128;
   }
   // Splits for about 16 (single rows: ragged lengths even out), 2 or 1 workgroups a
   // compute unit; of at least 256 keys, or 1024 where the tiles alone fill the chip
@@ -920,7 +920,9 @@ void launch_kernel(const AttnArgs& a, const Plan& p, hipStream_t stream) {
   } else if (p.rows == 128) {
     if (D <= 64)
       hipLaunchKernelGGL((attn_run_kernel<BF, 64, 4, ALIBI>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((attn_run_kernel<BF, 128, 4, ALIBI>), grid, dim3(256), 0, stream, a);
+    else if (D <= 128)
+      hipLaunchKernelGGL((attn_run_kernel<BF, 128, 4, ALIBI>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((attn_run_kernel<BF, 256, 4, ALIBI>), grid, dim3(256), 0, stream, a);
   } else {
     if (D <= 64)
       hipLaunchKernelGGL((attn_run_kernel<BF, 64, 8, ALIBI>), grid, dim3(512), 0, stream, a);

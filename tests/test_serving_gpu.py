@@ -420,6 +420,8 @@ WIDE_RUNS = [
     ([1025, 640, 511], [1025, 640, 400], 3, 2, 64, 128, 0, False),
     ([2100], [2100], 32, 1, 64, 64, 0, False),           # 256 rows a workgroup, not split
     ([1100, 1040], [400, 333], 6, 3, 16, 16, 0, False),
+    ([1100, 1040], [400, 333], 6, 3, 256, 64, 0, False),
+    ([2303], [129], 16, 1, 176, 128, 0, True),
     ([1100, 1040], [400, 333], 6, 3, 48, 64, 0, True),
 ]
 
