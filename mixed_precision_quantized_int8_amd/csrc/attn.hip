@@ -488,13 +488,18 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Att
   // A thread's value chunks run one tile behind its key chunks: step j takes keys of
   // tile j and values of tile j - 1.
   auto tile_of = [&](int u, int j) { return is_k(u) ? j : j - 1; };
+  // The last keys come first: with a position bias they have the highest scores, so
+  // that the maximum moves at the start and not in every tile.  (The incomplete page
+  // comes after them all: its values have no scale, and weights that were relative
+  // to them would lose bits where the codes' scales are small.)
+  auto tile0 = [&](int i) { return c_begin + (n_coded - 1 - i) * kApTile; };
   int pg[CPT];          // pages of the chunks to load next
   v4u raw[CPT];         // codes in flight
   auto load_page = [&](int u, int j) {
-    pg[u] = table[min(c_begin + max(tile_of(u, j), 0) * kApTile + sub[u], coded - 1) >> ps];
+    pg[u] = table[min(max(tile0(tile_of(u, j)) + sub[u], 0), coded - 1) >> ps];
   };
   auto load_chunk = [&](int u, int j) {   // after load_page(u, j)
-    const int in_page = (c_begin + tile_of(u, j) * kApTile) & (P - 1) & kApTile;
+    const int in_page = tile0(tile_of(u, j)) & (P - 1) & kApTile;
     const uint32_t page = exists(pg[u]) ? (uint32_t)pg[u] : 0u;
     raw[u] = *reinterpret_cast<const v4u*>(at0[u] + (uint64_t)page * page_step +
                                            (is_k(u) ? in_page * D : in_page));
@@ -507,8 +512,8 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Att
   int pm = -1;
   float ks = 0.0f, vs = 0.0f;
   auto load_meta_page = [&](int i) {
-    const int tok = c_begin + i * kApTile + 16 * lane;
-    pm = tok < coded ? table[tok >> ps] : -1;
+    const int tok = tile0(i) + 16 * lane;
+    pm = tok >= 0 && tok < coded ? table[tok >> ps] : -1;
   };
   bool meta_ok = false;
   auto load_scales = [&]() {
@@ -617,7 +622,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Att
   // before their use; `extra(n)` is more vector work for the first NV slots.
   constexpr int kAhead = 4, NV = 2 * ND;   // (8 pairs over NV, then over NK slots)
   auto half_tile = [&](int i, int k, auto extra) {
-    const int t0 = c_begin + i * kApTile;
+    const int t0 = tile0(i);
     uint32_t av = at_v + (uint32_t)((k ? i : i - 1) & 1) * kBuf;
     uint32_t ak = at_k + (uint32_t)((k ? i + 1 : i) & 1) * kBuf;
     asm volatile("" : "+v"(av), "+v"(ak));   // (offsets are formed here, not kept)
