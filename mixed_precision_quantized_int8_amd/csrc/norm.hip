@@ -9,7 +9,9 @@
 // exact fp32 product of two 16-bit values, and do not depend on the order of
 // the sum of squares.  One read of the row then serves the sum and the maximum.
 //
-// Bound by HBM: 2 + 2 bytes in, 2 + 1 bytes out per element.
+// Bound by HBM: 2 + 2 bytes in, 2 + 1 bytes out per element.  4096 x 14336 fp16 with
+// a residual: 77 us, 5.3 TB/s (a large copy reaches 5.15); below a few hundred rows
+// by latency: 1 x 4096 2.7 us, 1 x 14336 4.4 us.
 #include "half.h"
 #include "serve.h"
 
@@ -17,65 +19,85 @@ namespace i8l {
 
 constexpr int kNormChunk = 8;   // elements per 16-byte load
 
-// TPR threads per row, BS / TPR rows per workgroup; a thread holds NCH chunks of
-// its row, chunk t + i * TPR.  K % 16 == 0, K <= TPR * NCH * 8.
-template <int BS, int TPR, int NCH, bool BF>
-__global__ __launch_bounds__(BS) void rmsnorm_quant_kernel(
-    const uint16_t* X, const uint16_t* R, const uint16_t* __restrict__ W, int M, int K, float eps,
-    int8_t* __restrict__ Xq, float* __restrict__ sx, uint16_t* H) {   // H may be X or R
-  constexpr int RPB = BS / TPR;
-  const int t = threadIdx.x % TPR;
-  const int row = blockIdx.x * RPB + threadIdx.x / TPR;
-  const bool in = row < M;
-  const int nch = K / kNormChunk;
-  const size_t base = (size_t)(in ? row : 0) * K;
+// h of one chunk: x + r, rounded to the 16-bit type.
+template <bool BF>
+__device__ __forceinline__ v4u add_chunk(v4u x, v4u r) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    x[d] = pack2<BF>(to_f32<BF>((uint16_t)x[d]) + to_f32<BF>((uint16_t)r[d]),
+                     to_f32<BF>((uint16_t)(x[d] >> 16)) + to_f32<BF>((uint16_t)(r[d] >> 16)));
+  return x;
+}
+template <bool BF>
+__device__ __forceinline__ float half_of(const v4u& x, int e) {
+  return to_f32<BF>((uint16_t)(x[e >> 1] >> (16 * (e & 1))));
+}
+template <bool BF>
+__device__ __forceinline__ void chunk_stats(const v4u& h, const v4u& w, float* sum, float* top) {
+#pragma unroll
+  for (int e = 0; e < kNormChunk; ++e) {
+    const float hv = half_of<BF>(h, e);
+    *sum = __builtin_fmaf(hv, hv, *sum);
+    *top = __builtin_fmaxf(*top, __builtin_fabsf(hv * half_of<BF>(w, e)));
+  }
+}
+template <bool BF>
+__device__ __forceinline__ uint2 chunk_codes(const v4u& h, const v4u& w, float inv) {
+  int q[kNormChunk];
+#pragma unroll
+  for (int e = 0; e < kNormChunk; ++e)
+    q[e] = quant_code(half_of<BF>(h, e) * half_of<BF>(w, e), inv);
+  return make_uint2(pack4_i8(q[0], q[1], q[2], q[3]), pack4_i8(q[4], q[5], q[6], q[7]));
+}
 
-  // chunk i of this thread in a tensor of rows at `p`, zero past the row
-  auto load = [&](const uint16_t* p, int i) -> v4u {
-    const int c = t + i * TPR;
-    return in && c < nch ? *reinterpret_cast<const v4u*>(p + c * kNormChunk) : v4u{0, 0, 0, 0};
-  };
-  // wide rows read W again (from L2) rather than hold it: h alone is 4 NCH registers
-  constexpr bool kHoldW = NCH <= 4;
+// A workgroup of BS threads per row; a thread holds NCH chunks of it, chunk
+// t + i * BS (K <= BS * NCH * 8), or none (NCH 0: any K; the second pass reads the
+// row again, from h where that is stored, since h may be X or R).
+template <int BS, int NCH, bool BF>
+__global__ __launch_bounds__(BS) void rmsnorm_quant_kernel(
+    const uint16_t* X, const uint16_t* R, const uint16_t* __restrict__ W, int K, float eps,
+    int8_t* __restrict__ Xq, float* __restrict__ sx, uint16_t* H) {
+  constexpr bool kHold = NCH > 0;
+  constexpr bool kHoldW = kHold && NCH <= 4;   // wider rows read W again (from L2)
+  const int t = threadIdx.x, nch = K / kNormChunk;
+  const size_t base = (size_t)blockIdx.x * K;
   const v4u ones = BF ? v4u{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}
                       : v4u{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
-  v4u h[NCH], w[kHoldW ? NCH : 1];
-  float sum = 0.0f, top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) h[i] = load(X + base, i);
-  if constexpr (kHoldW) {
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) w[i] = W ? load(W, i) : ones;
-  }
-  if (R) {
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const v4u r = load(R + base, i);
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-        h[i][d] = pack2<BF>(to_f32<BF>((uint16_t)h[i][d]) + to_f32<BF>((uint16_t)r[d]),
-                            to_f32<BF>((uint16_t)(h[i][d] >> 16)) +
-                                to_f32<BF>((uint16_t)(r[d] >> 16)));
-    }
-  }
-  if (H) {
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * TPR;
-      if (in && c < nch) *reinterpret_cast<v4u*>(H + base + c * kNormChunk) = h[i];
-    }
-  }
-  auto half = [](const v4u& x, int e) -> float {
-    return to_f32<BF>((uint16_t)(x[e >> 1] >> (16 * (e & 1))));
+  auto at = [&](const uint16_t* p, int c) { return *reinterpret_cast<const v4u*>(p + c * kNormChunk); };
+  auto load = [&](const uint16_t* p, int i) -> v4u {   // chunk i of this thread, zero past the row
+    const int c = t + i * BS;
+    return c < nch ? at(p, c) : v4u{0, 0, 0, 0};
   };
+
+  v4u h[kHold ? NCH : 1], w[kHoldW ? NCH : 1];
+  float sum = 0.0f, top = 0.0f;
+  if constexpr (kHold) {
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const v4u wi = kHoldW ? w[kHoldW ? i : 0] : W ? load(W, i) : ones;
+    for (int i = 0; i < NCH; ++i) h[i] = load(X + base, i);
+    if constexpr (kHoldW) {
 #pragma unroll
-    for (int e = 0; e < kNormChunk; ++e) {
-      const float hv = half(h[i], e);
-      sum = __builtin_fmaf(hv, hv, sum);
-      top = __builtin_fmaxf(top, __builtin_fabsf(hv * half(wi, e)));
+      for (int i = 0; i < NCH; ++i) w[i] = W ? load(W, i) : ones;
+    }
+    if (R) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) h[i] = add_chunk<BF>(h[i], load(R + base, i));
+    }
+    if (H) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const int c = t + i * BS;
+        if (c < nch) *reinterpret_cast<v4u*>(H + base + c * kNormChunk) = h[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      chunk_stats<BF>(h[i], kHoldW ? w[kHoldW ? i : 0] : W ? load(W, i) : ones, &sum, &top);
+  } else {
+    for (int c = t; c < nch; c += BS) {
+      v4u x = at(X + base, c);
+      if (R) x = add_chunk<BF>(x, at(R + base, c));
+      if (H) *reinterpret_cast<v4u*>(H + base + c * kNormChunk) = x;
+      chunk_stats<BF>(x, W ? at(W, c) : ones, &sum, &top);
     }
   }
   // the row's sum and maximum
@@ -84,11 +106,10 @@ __global__ __launch_bounds__(BS) void rmsnorm_quant_kernel(
     sum += __shfl_xor(sum, off, 64);
     top = __builtin_fmaxf(top, __shfl_xor(top, off, 64));
   }
-  if constexpr (TPR > 64) {
-    static_assert(RPB == 1, "rows wider than a wave take the whole workgroup");
+  if constexpr (BS > 64) {
     __shared__ float s_sum[BS / 64], s_top[BS / 64];
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
+    const int wave = t >> 6;
+    if ((t & 63) == 0) {
       s_sum[wave] = sum;
       s_top[wave] = top;
     }
@@ -102,51 +123,56 @@ __global__ __launch_bounds__(BS) void rmsnorm_quant_kernel(
     }
   }
   const float inv = quant_scale(top);
+  if constexpr (kHold) {
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * TPR;
-    if (in && c < nch) {
-      const v4u wi = kHoldW ? w[kHoldW ? i : 0] : W ? load(W, i) : ones;
-      int q[kNormChunk];
-#pragma unroll
-      for (int e = 0; e < kNormChunk; ++e) q[e] = quant_code(half(h[i], e) * half(wi, e), inv);
-      uint2 o;
-      o.x = pack4_i8(q[0], q[1], q[2], q[3]);
-      o.y = pack4_i8(q[4], q[5], q[6], q[7]);
-      *reinterpret_cast<uint2*>(Xq + base + c * kNormChunk) = o;
+    for (int i = 0; i < NCH; ++i) {
+      const int c = t + i * BS;
+      if (c < nch)
+        *reinterpret_cast<uint2*>(Xq + base + c * kNormChunk) =
+            chunk_codes<BF>(h[i], kHoldW ? w[kHoldW ? i : 0] : W ? at(W, c) : ones, inv);
+    }
+  } else {
+    for (int c = t; c < nch; c += BS) {
+      v4u x = at((H ? H : X) + base, c);
+      if (!H && R) x = add_chunk<BF>(x, at(R + base, c));
+      *reinterpret_cast<uint2*>(Xq + base + c * kNormChunk) =
+          chunk_codes<BF>(x, W ? at(W, c) : ones, inv);
     }
   }
   // a non-finite value anywhere in the row makes the scale NaN
-  if (in && t == 0) sx[row] = top / __builtin_sqrtf(sum / (float)K + eps);
+  if (t == 0) sx[blockIdx.x] = top / __builtin_sqrtf(sum / (float)K + eps);
 }
 
-template <int BS, int TPR, int NCH>
+template <int BS, int NCH>
 static void launch_norm(const uint16_t* X, const uint16_t* R, const uint16_t* W, int M, int K,
                         float eps, bool bf16, int8_t* Xq, float* sx, uint16_t* H,
                         hipStream_t stream) {
-  const dim3 grid((M + BS / TPR - 1) / (BS / TPR)), block(BS);
   if (bf16)
-    hipLaunchKernelGGL((rmsnorm_quant_kernel<BS, TPR, NCH, true>), grid, block, 0, stream, X, R, W,
-                       M, K, eps, Xq, sx, H);
+    hipLaunchKernelGGL((rmsnorm_quant_kernel<BS, NCH, true>), dim3(M), dim3(BS), 0, stream, X, R, W,
+                       K, eps, Xq, sx, H);
   else
-    hipLaunchKernelGGL((rmsnorm_quant_kernel<BS, TPR, NCH, false>), grid, block, 0, stream, X, R,
-                       W, M, K, eps, Xq, sx, H);
+    hipLaunchKernelGGL((rmsnorm_quant_kernel<BS, NCH, false>), dim3(M), dim3(BS), 0, stream, X, R,
+                       W, K, eps, Xq, sx, H);
 }
 
+// Few chunks a thread: one row of 4096 takes 2.7 us with 512 threads, 3.1 with 256 and
+// 6.9 with 64, 4096 rows 25.3, 25.7 and 32.1; two chunks of 8192 elements 3.4 against
+// 4.1 us with four.  Up to 16384 elements four chunks cost nothing (14336: 77 us either
+// way) and 16384 x 4096 87 against 91 us.
 hipError_t launch_rmsnorm_quant(const uint16_t* X, const uint16_t* R, const uint16_t* W, int M,
                                 int K, float eps, bool bf16, int8_t* Xq, float* sx, uint16_t* H,
                                 hipStream_t stream) {
   const int nch = K / kNormChunk;
-#define I8L_NORM(BS, TPR, NCH) launch_norm<BS, TPR, NCH>(X, R, W, M, K, eps, bf16, Xq, sx, H, stream)
-  if (nch <= 64) I8L_NORM(256, 64, 1);
-  else if (nch <= 128) I8L_NORM(256, 64, 2);
-  else if (nch <= 256) I8L_NORM(256, 256, 1);
-  else if (nch <= 512) I8L_NORM(256, 256, 2);
-  else if (nch <= 1024) I8L_NORM(256, 256, 4);
-  else if (nch <= 2048) I8L_NORM(512, 512, 4);
-  else if (nch <= 4096) I8L_NORM(1024, 1024, 4);
-  else if (nch <= 8192) I8L_NORM(1024, 1024, 8);
-  else I8L_NORM(1024, 1024, 17);   // K <= 133136 (the layer's largest): 16642 chunks
+#define I8L_NORM(BS, NCH) launch_norm<BS, NCH>(X, R, W, M, K, eps, bf16, Xq, sx, H, stream)
+  if (nch <= 64) I8L_NORM(64, 1);
+  else if (nch <= 128) I8L_NORM(128, 1);
+  else if (nch <= 256) I8L_NORM(256, 1);
+  else if (nch <= 512) I8L_NORM(512, 1);
+  else if (nch <= 1024) I8L_NORM(512, 2);
+  else if (nch <= 2048) I8L_NORM(512, 4);
+  else if (nch <= 4096) I8L_NORM(1024, 4);
+  else if (nch <= 8192) I8L_NORM(1024, 8);
+  else I8L_NORM(1024, 0);   // past the registers of 16 waves
 #undef I8L_NORM
   return hipGetLastError();
 }

@@ -91,6 +91,24 @@ def test_rmsnorm_quant_ties_and_in_place(lib):
     same(q2, O.rmsnorm_quant(X + 1)[0])
 
 
+@pytest.mark.parametrize("K", [64, 4096, 57344, 65552])
+def test_rmsnorm_quant_writes_h_over_its_inputs(lib, K):
+    """h over the residual, and over X: the same codes and scales as into a tensor of
+    its own (the widest rows are read twice)."""
+    g = gen(K)
+    X, R = (torch.randn((3, K), generator=g).half().cuda() for _ in range(2))
+    W = (1 + 0.2 * torch.randn(K, generator=g)).half().cuda()
+    q, s, h = lib.rmsnorm_quant(X, W, residual=R)
+    for over in ("residual", "X"):
+        x, r = X.clone(), R.clone()
+        out = r if over == "residual" else x
+        q2, s2, h2 = lib.rmsnorm_quant(x, W, residual=r, residual_out=out)
+        assert h2.data_ptr() == out.data_ptr()
+        same(h2, h)
+        same(q2, q)
+        same(s2, s)
+
+
 def test_rmsnorm_quant_non_finite_rows(lib):
     """A NaN or an infinity shows in its own row's scale and in no other."""
     X = torch.randn((4, 256), generator=gen(1)).half()
