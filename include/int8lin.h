@@ -374,8 +374,8 @@ typedef struct {
 
 /* Writes the call's rows as the last tokens of their sequences: row j of a
  * sequence with m rows is its token lengths[i] - m + j.  Tokens before them in
- * the same page must be in the slot (written there by earlier calls).  Pages and
- * slots of different sequences must differ.
+ * the same page must be in the slot (written there by earlier calls).  Sequences
+ * may share complete pages, not slots or pages that a call writes.
  *   k, v   [rows][heads][head_dim] dtype; element (t, h, d) at
  *          t * token_stride + h * head_stride + d (strides in elements,
  *          multiples of 8; pointers 16-byte aligned)

@@ -6,6 +6,10 @@ libint8lin.so; torch supplies device memory and the current stream.
 
     Wq, sw = quantize_weight(W)              # W fp16 [K][N] (Y = X @ W)
     Y = linear(X, Wq, sw, W, threshold=6.0)  # X fp16 [M][K] -> Y fp16 [M][N]
+
+Serving around the layer (serving.py: norm to codes, product of codes, an 8-bit
+key/value cache, attention over it) is reached from here too; decoder.py runs
+it together.
 """
 from __future__ import annotations
 

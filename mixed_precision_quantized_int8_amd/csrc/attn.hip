@@ -1,5 +1,6 @@
-// Attention over the 8-bit key/value cache: single queries and short runs of
-// them against long contexts.
+// Attention over the 8-bit key/value cache: attn_decode_kernel for single queries
+// and short calls, attn_run_kernel for runs of queries, attn_join_kernel for keys
+// that were split over workgroups.
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j - slope (i - j))
 // over the keys j <= i (and i - j < window) of the sequence, k_j = ks c^k_j and
@@ -10,7 +11,9 @@
 //   o = sum_j w_j c^v_j / sum_j w_j / vs_j,
 // so the product on the matrix cores runs on the codes themselves, and the
 // rounding of w_j to 16 bits is relative to the largest contribution.  Codes
-// are exact in fp16 and bf16; m and the sums are fp32.
+// are exact in fp16 and bf16; m and the sums are fp32.  The tokens of the incomplete
+// page have 16-bit values and no scale; every kernel takes them last, since weights
+// relative to them would lose bits where the codes' scales are small.
 #include <algorithm>
 #include <type_traits>
 
@@ -77,6 +80,17 @@ __device__ __forceinline__ void say_empty(const AttnArgs& a, int b, int h, int r
 // 16 (i / 4) + 4 j + i % 4, so that a lane's sixteen scores are neighbours, lie
 // in one page (P >= 16), and are, in order, the lane's operand for the second
 // product, whose V^T operand is then 16 contiguous bytes of the [D][P] page.
+//
+// Bound by the read of the codes: four waves take a tile of 64 keys each, straight
+// from memory to registers (no wave shares a key with another, so nothing passes
+// through LDS), with the next tile's codes in flight; results of the waves meet in
+// LDS at the end.  The matrix cores run 16 columns for however many rows there are;
+// converting the codes is the larger part of the vector work, a few times below the
+// memory's rate.  One sequence of 131072 tokens, 112 heads of 128: 3.76 GB in
+// 615 us, 6.1 TB/s; 64 sequences of 2 - 8 thousand, 32 heads on 8: 684 MB in 156 us,
+// 4.4 TB/s (a large copy reaches 5.15); 100 tokens, 16 heads of 64: 7.4 us, latency.
+// A third workgroup a compute unit (168 registers) was slower: 167 and 743 us; two
+// blocks of 16 rows a wave too (32 rows, 64 heads, 65536 keys: 321 against 303 us).
 //
 // DP: head dimension padded to a multiple of 64 (64, 128, 256).
 template <bool BF, int DP, bool ALIBI>
@@ -384,6 +398,15 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
 // are runs of eight keys, the order in which the second product takes them.
 // The running maximum moves only when a score passes it by 8 (in log2): the
 // weights then stay below 2^8 and most tiles leave O alone.
+//
+// Bound by the matrix cores under the board's power limit: 4096 queries over 8192
+// tokens, 32 heads of 128 on 8, in 411 us, 1000 TFLOP/s (a large fp16 product reaches
+// 1080 on the same card); heads of 64 run at half that, on the exponentials.  What
+// carried it there: products and vector work in alternating slots (half_tile) with
+// staging that has no branches (638 -> 455 us; two groups of waves half a step
+// apart, with barriers, had been slower: 701); eight waves of 32 rows rather than
+// four of 64 (which left one wave a SIMD waiting: 752 us; with heads of 256 there is
+// no room for more, and the slots keep it at 760 TFLOP/s).
 constexpr int kApTile = 64;
 constexpr float kApSlack = 8.0f;
 
