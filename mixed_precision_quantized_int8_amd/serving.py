@@ -59,6 +59,26 @@ def _dense(t, dtype, shape, device, name):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _result(t, dtype, shape, device, name):
+    """(tensor, pointer) to write a result to: the caller's, or a new one."""
+    if t is not None:
+        return t, _dense(t, dtype, shape, device, name)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    return t, t.data_ptr()
+
+
+def _scratch(workspace, nbytes, device):
+    """(pointer, bytes) of the caller's workspace, or of a new one; the tensor lives
+    until its memory may be given to later work of the same stream."""
+    if workspace is None:
+        if not nbytes:
+            return None, None, 0
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
+    n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    return workspace, _dense(workspace, torch.uint8, (n,), device, "workspace"), n
+
+
 def _half_type(t, name, dims):
     """The dtype code of a GPU tensor in fp16 or bf16 with this many dimensions."""
     if not isinstance(t, torch.Tensor):
@@ -88,18 +108,13 @@ def rmsnorm_quant(X, weight=None, residual=None, eps=1e-5, Xq=None, sx=None, res
     x = _dense(X, dt, (M, K), None, "X")
     w = None if weight is None else _dense(weight, dt, (K,), dev, "weight")
     r = None if residual is None else _dense(residual, dt, (M, K), dev, "residual")
-    if Xq is None:
-        Xq = torch.empty((M, K), dtype=torch.int8, device=dev)
-    if sx is None:
-        sx = torch.empty((M,), dtype=torch.float32, device=dev)
+    Xq, qp = _result(Xq, torch.int8, (M, K), dev, "Xq")
+    sx, sp = _result(sx, torch.float32, (M,), dev, "sx")
     h, hp = X, None
     if residual_out is not None or residual is not None:
-        h = residual_out if residual_out is not None else torch.empty_like(X)
-        hp = _dense(h, dt, (M, K), dev, "residual_out")
+        h, hp = _result(residual_out, dt, (M, K), dev, "residual_out")
     with _on(dev):
-        check(lib().int8_rmsnorm_quant(
-            x, r, w, M, K, float(eps), code, _dense(Xq, torch.int8, (M, K), dev, "Xq"),
-            _dense(sx, torch.float32, (M,), dev, "sx"), hp, _stream(dev)))
+        check(lib().int8_rmsnorm_quant(x, r, w, M, K, float(eps), code, qp, sp, hp, _stream(dev)))
     return Xq, sx, h
 
 
@@ -120,20 +135,13 @@ def linear_codes(Xq, sx, Wq, sw, bias=None, out=None, workspace=None):
     xp = _dense(Xq, torch.int8, (M, K), None, "Xq")
     wp = _dense(Wq, torch.int8, (N, K), dev, "Wq")
     b = None if bias is None else _dense(bias, torch.float16, (N,), dev, "bias")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=dev)
-    if workspace is None and M > 64:
-        n = int(lib().i8l_codes_workspace_bytes(M, K, N))
-        workspace = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
-    ws, nb = None, 0
-    if workspace is not None:
-        nb = workspace.numel()
-        ws = _dense(workspace, torch.uint8, (nb,), dev, "workspace")
+    out, op = _result(out, torch.float16, (M, N), dev, "out")
+    need = 0 if workspace is not None or M <= 64 else int(lib().i8l_codes_workspace_bytes(M, K, N))
+    hold, ws, nb = _scratch(workspace, need, dev)
     with _on(dev):
         check(lib().int8_linear_codes(
             xp, _dense(sx, torch.float32, (M,), dev, "sx"), M, K, wp,
-            _dense(sw, torch.float32, (N,), dev, "sw"), N, b,
-            _dense(out, torch.float16, (M, N), dev, "out"), ws, nb, _stream(dev)))
+            _dense(sw, torch.float32, (N,), dev, "sw"), N, b, op, ws, nb, _stream(dev)))
     return out
 
 
@@ -150,8 +158,8 @@ class KVCache:
     P is 16, 32, 64 or 128; head_dim a multiple of 16 up to 256.
     """
 
-    __slots__ = ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "n_pages",
-                 "n_slots", "heads", "page_size", "head_dim", "dtype", "device", "_struct")
+    __slots__ = ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "heads",
+                 "page_size", "head_dim", "dtype", "device", "_struct")
 
     def __init__(self, k_codes, v_codes, k_scale, v_scale, k_tail, v_tail):
         code = _half_type(k_tail, "k_tail", 4)
@@ -168,8 +176,16 @@ class KVCache:
             _dense(v_tail, dt, (slots, H, D, P), dev, "v_tail"), n, slots, H, D, P, code)
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.k_tail, self.v_tail = k_tail, v_tail
-        self.n_pages, self.n_slots, self.heads, self.page_size, self.head_dim = n, slots, H, P, D
+        self.heads, self.page_size, self.head_dim = H, P, D
         self.dtype, self.device = dt, dev
+
+    @property
+    def n_pages(self):
+        return self._struct.n_pages
+
+    @property
+    def n_slots(self):
+        return self._struct.n_slots
 
 
 def new_cache(n_pages, n_slots, heads, head_dim, page_size=64, dtype=torch.float16,
@@ -255,15 +271,13 @@ def cache_read(cache, page_table, lengths, cu, total, slots=None, max_len=None, 
     shape = (int(total), cache.heads, cache.head_dim)
     if cu is None:
         raise ValueError("cu must name the first row of each sequence")
-    if out is None:
-        out = tuple(torch.empty(shape, dtype=cache.dtype, device=cache.device) for _ in range(2))
-    k, v = out
+    k, v = (None, None) if out is None else out
+    k, kp = _result(k, cache.dtype, shape, cache.device, "k")
+    v, vp = _result(v, cache.dtype, shape, cache.device, "v")
     if max_len is None:
         max_len = s.max_pages * cache.page_size
     with _on(cache.device):
-        check(lib().int8_cache_read(_byref(cache._struct), _byref(s),
-                                    _dense(k, cache.dtype, shape, cache.device, "k"),
-                                    _dense(v, cache.dtype, shape, cache.device, "v"), shape[0],
+        check(lib().int8_cache_read(_byref(cache._struct), _byref(s), kp, vp, shape[0],
                                     int(max_len), _stream(cache.device)))
     return k, v
 
@@ -298,19 +312,14 @@ def cache_attention(q, cache, page_table, lengths, cu=None, slots=None, max_q=No
         max_q = 1 if cu is None else max(rows, 1)
     if max_len is None:
         max_len = s.max_pages * cache.page_size
-    if out is None:
-        out = torch.empty((rows, heads, D), dtype=q.dtype, device=dev)
-    if workspace is None:
-        n = attention_workspace_bytes(cache, s.n, heads, max_q, max_len, window)
-        workspace = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
-    ws, nb = None, 0
-    if workspace is not None:
-        nb = workspace.numel()
-        ws = _dense(workspace, torch.uint8, (nb,), dev, "workspace")
+    out, op = _result(out, q.dtype, (rows, heads, D), dev, "out")
+    need = 0 if workspace is not None else \
+        attention_workspace_bytes(cache, s.n, heads, max_q, max_len, window)
+    hold, ws, nb = _scratch(workspace, need, dev)
     with _on(dev):
         check(lib().int8_cache_attention(
             _byref(cache._struct), _byref(s), qp, qt, qh, heads, rows, int(max_q), int(max_len),
             float(D ** -0.5 if scale is None else scale), int(window),
             None if alibi is None else _dense(alibi, torch.float32, (heads,), dev, "alibi"),
-            _dense(out, q.dtype, (rows, heads, D), dev, "out"), ws, nb, _stream(dev)))
+            op, ws, nb, _stream(dev)))
     return out
