@@ -100,7 +100,14 @@ __global__ __launch_bounds__(kCtThreads, 1) void codes_tile_kernel(CodesArgs a) 
   int8_t* const sB = smem + kCtRing * kCtA;
   const int M = a.M, N = a.N, K = a.K;
   const int tiles_n = (N + kCtN - 1) / kCtN, tiles = tiles_n * ((M + kCtM - 1) / kCtM);
-  const int tile = blockIdx.x % tiles, split = blockIdx.x / tiles;
+  // Workgroup b runs on XCD b % 8.  Narrow products give each XCD a run of
+  // neighbouring tiles, whose rows of codes its L2 then reads once (4096 x 14336 x 256:
+  // 42 -> 36 us); wide ones, tile by tile, a share of the weight (1024 x 4096 x 1024:
+  // 16.5 against 18.9).
+  const int items = tiles * a.n_split;
+  const int item = tiles_n > 8 ? (int)blockIdx.x : blockIdx.x % 8 * ((items + 7) / 8) + blockIdx.x / 8;
+  if (item >= items) return;
+  const int tile = item % tiles, split = item / tiles;
   const int m0 = tile / tiles_n * kCtM, n0 = tile % tiles_n * kCtN;
   const int nk = (K + kCtK - 1) / kCtK;
   const int s0 = (int)((int64_t)split * nk / a.n_split), s1 = (int)((int64_t)(split + 1) * nk / a.n_split);
@@ -243,7 +250,8 @@ hipError_t launch_codes(CodesArgs a, const CodesPlan& p, const int32_t* zeros, h
   if (p.kind == CodesPlan::kTiles) {
     a.n_split = a.part ? p.n_split : 1;
     const int tiles = ((a.M + kCtM - 1) / kCtM) * ((a.N + kCtN - 1) / kCtN);
-    hipLaunchKernelGGL(codes_tile_kernel, dim3(tiles * a.n_split), dim3(kCtThreads), 0, stream, a);
+    hipLaunchKernelGGL(codes_tile_kernel, dim3((tiles * a.n_split + 7) / 8 * 8), dim3(kCtThreads), 0,
+                       stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_split == 1) return e;
     const size_t quads = ((size_t)a.M * a.N + 3) / 4;
