@@ -339,9 +339,14 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
     }
   };
 
-  if (end > coded && coded >= begin)
-    for (int t0 = (coded & ~(kAdTile - 1)) + wave * kAdTile; t0 < end; t0 += kAdWaves * kAdTile)
+  if (end > coded && coded >= begin) {
+    // The waves whose turn comes after the complete pages' last tile: 100 tokens (one
+    // tile of complete pages, one of the tail) 7.4 -> 5.8 us.
+    const int n_tiles = max(c_end - (c0 - wave * kAdTile) + kAdTile - 1, 0) / kAdTile;
+    const int turn = (wave - n_tiles) & (kAdWaves - 1);
+    for (int t0 = (coded & ~(kAdTile - 1)) + turn * kAdTile; t0 < end; t0 += kAdWaves * kAdTile)
       tail_tile(t0);
+  }
 
   // the four waves' results together
   l = xsum16(l);
