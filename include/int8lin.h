@@ -339,7 +339,8 @@ i8l_status int8_linear_codes(const int8_t *Xq, const float *sx, int64_t M, int64
  * have one scale for each page and kv head.
  *   scale = fl32(absmax / 127) over the page's page_size * head_dim values,
  *   code = clamp(round_half_away(x * fl32(127 / absmax)), -127, 127),
- *   value = code * scale   (a page with a NaN or an infinity: scale NaN).
+ *   value = code * scale   (a page with a NaN or an infinity: scale NaN; one
+ *   whose absmax is below 2^-93: scale and codes 0).
  * A page's codes are made when its last token arrives; the tokens of a
  * sequence's last, incomplete page are kept in 16 bits in the sequence's slot.
  * So no value is rounded twice, and what the cache holds does not depend on how

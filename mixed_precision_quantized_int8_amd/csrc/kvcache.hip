@@ -10,7 +10,9 @@
 // tokens are kept in 16 bits in the sequence's tail slot.  So no value is ever
 // rounded twice, and what the cache holds depends on the tokens alone, not on
 // how many calls brought them.  A page that holds a NaN or an infinity gets the
-// scale NaN (every value of it then reads as NaN).
+// scale NaN (every value of it then reads as NaN); one of bf16 values that are all
+// below 2^-93 counts as zeros, which keeps 127 * 2^16 / absmax and attention's
+// 1 / scale inside fp32.
 //
 // Keys are stored [token][D], values [D][token]: each is contiguous along the
 // dimension that attention sums over.
@@ -144,7 +146,8 @@ __device__ __forceinline__ void write_page(const Cache& c, const Sequences& s, c
       for (int i = 0; i < BS / 64; ++i) bits = max(bits, red[i]);
     }
     const bool finite = bits < (BF ? 0x7f80u : 0x7c00u);
-    const float top = to_f32<BF>((uint16_t)bits);
+    const float absmax = to_f32<BF>((uint16_t)bits);
+    const float top = absmax < kLeastMax ? 0.0f : absmax;
     const float inv65 = (finite ? quant_scale(top) : 0.0f) * 65536.0f;
     int8_t* out = (V ? c.vc : c.kc) + ((size_t)(page_ok ? page : 0) * c.H + h) * P * D;
 #pragma unroll

@@ -13,6 +13,7 @@ import math
 import torch
 
 F32, F64 = torch.float32, torch.float64
+LEAST = 2.0 ** -93   # an absmax below this counts as 0
 
 
 def codes(x, absmax):
@@ -53,6 +54,7 @@ class Store:
         top = x.abs().to(F32).max() if torch.isfinite(x.to(F32)).all() else torch.tensor(math.inf)
         if not math.isfinite(float(top)):
             return torch.zeros(x.shape, dtype=torch.int8), torch.tensor(math.nan, dtype=F32)
+        top = torch.where(top < LEAST, torch.zeros_like(top), top)
         return codes(x, top), top / torch.tensor(127.0, dtype=F32)
 
     def sequence(self, x):

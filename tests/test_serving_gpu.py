@@ -331,6 +331,22 @@ def test_cache_zero_and_non_finite_pages(lib):
     assert bool(k[64:80, 0].isnan().all()) and not bool(k[64:80, 1].isnan().any())
 
 
+@pytest.mark.parametrize("e", [-126, -120, -112, -105, -94, -93, -92, -60, 120])
+def test_cache_pages_of_very_small_and_large_values(lib, e):
+    """bf16 pages over the type's range: below 2^-93 zeros, from there on codes as
+    anywhere (of 127 * 2^16 / absmax nothing overflows)."""
+    w = World(lib, [48], 2, 32, 16, "bf16", seed=e + 200, fill=False)
+    for x in (w.k[0], w.v[0]):
+        x[16:32] = (torch.rand((16, 2, 32), generator=gen(5)) * 2 - 1).to(w.dt) * 2.0 ** e
+        x[20, :, 3] = 2.0 ** e
+    w.write([0], w.lens)
+    w.check_content()
+    k, v = lib.cache_read(w.cache, w.table, w.lengths, w.cu(w.lens), 48, slots=w.slots)
+    (k0, v0, _), = w.stored()
+    same(k, k0.to(w.dt))
+    same(v, v0.to(w.dt))
+
+
 def test_cache_ignores_pages_and_slots_outside(lib):
     """A table entry or slot outside the cache is skipped: nothing else changes."""
     w = World(lib, [48, 20], 1, 64, 16, "fp16", seed=4)
