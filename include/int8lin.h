@@ -313,8 +313,9 @@ typedef enum { I8L_FP16 = 0, I8L_BF16 = 1 } i8l_dtype;
  *   h         [M][K]  out, or NULL (not stored); may be X or residual
  *   Xq        int8 [M][K] out; sx fp32 [M] out
  *   eps       >= 0
- * Statistics in fp32.  A row with a non-finite h or g gets the scale NaN (or
- * infinity where only g overflowed).  M and K as for int8_linear. */
+ * Statistics in fp32.  A row with a NaN, or an infinity in h, gets the scale NaN
+ * (infinity where only g has one); a row whose a is below 2^-93 gets codes and
+ * scale 0.  M and K as for int8_linear. */
 i8l_status int8_rmsnorm_quant(const uint16_t *X, const uint16_t *residual,
                               const uint16_t *weight, int64_t M, int64_t K, float eps,
                               int dtype, int8_t *Xq, float *sx, uint16_t *h, void *stream);

@@ -8,8 +8,8 @@ namespace i8l {
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-// A page whose largest magnitude is below this counts as zeros (fp16 values are
-// 2^-24 and above).
+// A page or row whose largest magnitude is below this counts as zeros (fp16 values
+// are 2^-24 and above).
 constexpr float kLeastMax = 0x1p-93f;
 
 // fp16 (BF false) or bf16 (BF true) bits to fp32 and back, rounding to nearest

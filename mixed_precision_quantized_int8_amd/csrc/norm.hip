@@ -8,6 +8,9 @@
 // of the codes and only enters the scale: the codes are decided on g, the
 // exact fp32 product of two 16-bit values, and do not depend on the order of
 // the sum of squares.  One read of the row then serves the sum and the maximum.
+// The maximum is taken over the bits of |g|, whose order puts infinities and NaNs
+// last, so that either shows in sx.  A row whose a is below 2^-93 counts as zeros
+// (127 / a stays finite).
 //
 // Bound by HBM: 2 + 2 bytes in, 2 + 1 bytes out per element.  4096 x 14336 fp16 with
 // a residual: 77 us, 5.3 TB/s (a large copy reaches 5.15); below a few hundred rows
@@ -33,12 +36,13 @@ __device__ __forceinline__ float half_of(const v4u& x, int e) {
   return to_f32<BF>((uint16_t)(x[e >> 1] >> (16 * (e & 1))));
 }
 template <bool BF>
-__device__ __forceinline__ void chunk_stats(const v4u& h, const v4u& w, float* sum, float* top) {
+__device__ __forceinline__ void chunk_stats(const v4u& h, const v4u& w, float* sum,
+                                            uint32_t* top) {
 #pragma unroll
   for (int e = 0; e < kNormChunk; ++e) {
     const float hv = half_of<BF>(h, e);
     *sum = __builtin_fmaf(hv, hv, *sum);
-    *top = __builtin_fmaxf(*top, __builtin_fabsf(hv * half_of<BF>(w, e)));
+    *top = max(*top, __builtin_bit_cast(uint32_t, hv * half_of<BF>(w, e)) & 0x7fffffffu);
   }
 }
 template <bool BF>
@@ -70,7 +74,8 @@ __global__ __launch_bounds__(BS) void rmsnorm_quant_kernel(
   };
 
   v4u h[kHold ? NCH : 1], w[kHoldW ? NCH : 1];
-  float sum = 0.0f, top = 0.0f;
+  float sum = 0.0f;
+  uint32_t bits = 0;
   if constexpr (kHold) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) h[i] = load(X + base, i);
@@ -91,37 +96,38 @@ __global__ __launch_bounds__(BS) void rmsnorm_quant_kernel(
     }
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
-      chunk_stats<BF>(h[i], kHoldW ? w[kHoldW ? i : 0] : W ? load(W, i) : ones, &sum, &top);
+      chunk_stats<BF>(h[i], kHoldW ? w[kHoldW ? i : 0] : W ? load(W, i) : ones, &sum, &bits);
   } else {
     for (int c = t; c < nch; c += BS) {
       v4u x = at(X + base, c);
       if (R) x = add_chunk<BF>(x, at(R + base, c));
       if (H) *reinterpret_cast<v4u*>(H + base + c * kNormChunk) = x;
-      chunk_stats<BF>(x, W ? at(W, c) : ones, &sum, &top);
+      chunk_stats<BF>(x, W ? at(W, c) : ones, &sum, &bits);
     }
   }
   // the row's sum and maximum
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) {
     sum += __shfl_xor(sum, off, 64);
-    top = __builtin_fmaxf(top, __shfl_xor(top, off, 64));
+    bits = max(bits, (uint32_t)__shfl_xor((int)bits, off, 64));
   }
   if constexpr (BS > 64) {
-    __shared__ float s_sum[BS / 64], s_top[BS / 64];
+    __shared__ float s_sum[BS / 64];
+    __shared__ uint32_t s_top[BS / 64];
     const int wave = t >> 6;
     if ((t & 63) == 0) {
       s_sum[wave] = sum;
-      s_top[wave] = top;
+      s_top[wave] = bits;
     }
     __syncthreads();
     sum = 0.0f;
-    top = 0.0f;
 #pragma unroll
     for (int i = 0; i < BS / 64; ++i) {
       sum += s_sum[i];
-      top = __builtin_fmaxf(top, s_top[i]);
+      bits = max(bits, s_top[i]);
     }
   }
+  const float a = __builtin_bit_cast(float, bits), top = a < kLeastMax ? 0.0f : a;
   const float inv = quant_scale(top);
   if constexpr (kHold) {
 #pragma unroll
@@ -139,8 +145,9 @@ __global__ __launch_bounds__(BS) void rmsnorm_quant_kernel(
           chunk_codes<BF>(x, W ? at(W, c) : ones, inv);
     }
   }
-  // a non-finite value anywhere in the row makes the scale NaN
-  if (t == 0) sx[blockIdx.x] = top / __builtin_sqrtf(sum / (float)K + eps);
+  // a NaN, or an infinity in h, makes the scale NaN; a row of zeros has 0 for any eps
+  if (t == 0)
+    sx[blockIdx.x] = top == 0.0f ? 0.0f : top / __builtin_sqrtf(sum / (float)K + eps);
 }
 
 template <int BS, int NCH>

@@ -30,8 +30,10 @@ def rmsnorm_quant(X, weight=None, residual=None, eps=1e-5):
     h = X if residual is None else (X.to(F32) + residual.to(F32)).to(X.dtype)
     g = h.to(F32) if weight is None else h.to(F32) * weight.to(F32)
     top = g.abs().amax(dim=1, keepdim=True)
+    top = torch.where(top < LEAST, torch.zeros_like(top), top)
     rms = torch.sqrt(h.to(F64).square().mean(dim=1) + eps)
-    return codes(g, top), top[:, 0].to(F64) / rms, h
+    sx = top[:, 0].to(F64) / rms
+    return codes(g, top), torch.where(top[:, 0] == 0, torch.zeros_like(sx), sx), h
 
 
 def linear_codes(Xq, sx, Wq, sw, bias=None):

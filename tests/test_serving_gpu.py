@@ -121,6 +121,42 @@ def test_rmsnorm_quant_non_finite_rows(lib):
         same(s[i], clean[1][i])
 
 
+@pytest.mark.parametrize("K", [256, 4096, 65552])
+def test_rmsnorm_quant_non_finite_weight(lib, K):
+    """A NaN in the weight shows in every row's scale, an infinity too."""
+    X = torch.rand((3, K), generator=gen(K)).half() + 1
+    for bad in (math.nan, math.inf, -math.inf):
+        W = torch.ones(K).half()
+        W[K - 5] = bad
+        _, s, h = lib.rmsnorm_quant(X.cuda(), W.cuda())
+        same(h, X)
+        assert not bool(s.isfinite().any())
+        assert bool(s.isnan().all()) or not math.isnan(bad)
+
+
+def test_rmsnorm_quant_very_small_rows(lib):
+    """bf16 rows over the small end of the type's range: below 2^-93 codes and scale 0;
+    a zero among them is code 0 everywhere, also with eps = 0."""
+    X = torch.rand((6, 512), generator=gen(8)) * 2 - 1
+    X[:, 5], X[:, 9] = 1.0, 0.0
+    X = X.bfloat16()
+    W = torch.ones(512)
+    X[4] = 0
+    for i, e in enumerate((-126, -120, -94, -92)):   # (powers of two: exact)
+        W2 = (W * 2.0 ** (e // 2)).bfloat16()
+        Y = X.clone()
+        Y[:4] = Y[:4] * 2.0 ** (e - e // 2)
+        for eps in (0.0, 1e-5):
+            q, s, h = lib.rmsnorm_quant(Y.cuda(), W2.cuda(), eps=eps)
+            q0, s0, _ = O.rmsnorm_quant(Y, W2, None, eps)
+            same(q, q0)
+            # squares of rows near 2^-63 are fp32 subnormals, and the row's own eps-free
+            # root with them: the scale is held to eps > 0, and zeros to both
+            assert bool((s.cpu()[s0 == 0] == 0).all())
+            if eps:
+                assert bool(((s.cpu().double() - s0).abs() <= 1e-5 * s0 + 2.0 ** -126).all())
+
+
 # ---- product --------------------------------------------------------------------
 
 CODES = [(1, 16, 1), (1, 4096, 1000), (8, 4096, 16384), (16, 1024, 33), (17, 272, 130), (64, 2064, 1300),
