@@ -146,8 +146,9 @@ __global__ __launch_bounds__(kCtThreads, 1) void codes_tile_kernel(CodesArgs a) 
   load_step(s0 + 2);
   const int ra = wm + l32, rw = wn + l32;
   for (int s = s0; s < s1; ++s) {
-    // vmcnt(6): step s has landed, the six loads of steps s + 1 and s + 2 may fly
-    __builtin_amdgcn_s_waitcnt(6 | (0x7 << 4) | (0xf << 8));
+    // vmcnt(6): step s has landed, the six loads of steps s + 1 and s + 2 may fly;
+    // lgkmcnt(0): step s - 1 has been read from the slot that step s + 3 goes to
+    __builtin_amdgcn_s_waitcnt(6 | (0x7 << 4));
     asm volatile("s_barrier" ::: "memory");   // for every wave; step s - 1 is consumed
     load_step(s + 3);
     const int slot = s % kCtRing;
