@@ -230,9 +230,10 @@ i8l_status check_count(const char* fn, const char* name, int64_t v, int64_t lo, 
   return I8L_OK;
 }
 
-// Workgroups of a launch: one for each page, head, and keys or values.
+// Workgroups of a launch: one for each page, head, and keys or values, of up to 256
+// threads; the threads along an axis are counted in 32 bits.
 i8l_status check_pages(const char* fn, const i8l::Cache& c, int64_t tokens) {
-  if (((tokens >> c.ps) + 2) * 2 * c.H > INT32_MAX)
+  if (((tokens >> c.ps) + 2) * 2 * c.H >= 1 << 24)
     return fail(I8L_ERR_INVALID_ARG, fn, "%lld tokens of %d heads are too many for one call",
                 (long long)tokens, c.H);
   return I8L_OK;
@@ -292,7 +293,7 @@ I8L_API i8l_status int8_cache_read(const i8l_kv_cache* cache, const i8l_sequence
   CHECK(check_count(fn, "rows", rows, 0, kMaxRows));
   CHECK(check_count(fn, "max_len", max_len, 0, kMaxTokens));
   if (rows == 0 || max_len == 0 || s.B == 0 || s.max_pages == 0) return ok();
-  max_len = std::min(max_len, (int64_t)s.max_pages << c.ps);
+  max_len = std::min(std::min(max_len, rows), (int64_t)s.max_pages << c.ps);
   CHECK(check_pages(fn, c, max_len));
   CHECK_PTR(k, 16);
   CHECK_PTR(v, 16);

@@ -129,6 +129,18 @@ def test_cache_calls_refuse(i8l):
     assert L.i8l_attention_workspace_bytes(ref(cache_struct(head_dim=24)), 2, 8, 1, 100000, 0) == 0
 
 
+def test_cache_calls_refuse_launches_that_are_too_large(i8l):
+    """2^24 workgroups (pages x heads x 2) and more of one sequence in one call."""
+    L, ref = i8l.lib(), ctypes.byref
+    c, s = cache_struct(heads=4096), seqs_struct(max_pages=1 << 20)
+    most = 2046 * 16 + 16   # pages + 2 reach 2^24 / (2 * 4096) = 2048 with the last token
+    assert L.int8_cache_write(ref(c), ref(s), P16, 1 << 18, 64, P16, 1 << 18, 64, most, most,
+                              None) == INVALID
+    assert "too many" in i8l.last_error()
+    assert L.int8_cache_read(ref(c), ref(s), P16, P16, most, 1 << 23, None) == INVALID
+    assert "too many" in i8l.last_error()
+
+
 def test_wrappers_refuse(i8l):
     X = torch.zeros((2, 64), dtype=torch.float16)
     with pytest.raises(ValueError, match="on a GPU"):
