@@ -416,7 +416,9 @@ size_t i8l_attention_workspace_bytes(const i8l_kv_cache *cache, int64_t n, int64
  *          not depend on it beyond the order of sums)
  *   workspace  i8l_attention_workspace_bytes(...) bytes, 16-byte aligned
  * Scores, softmax statistics and sums in fp32; the weights are rounded to
- * dtype, relative to the row's largest contribution, for the matrix cores. */
+ * dtype, relative to the row's largest contribution, for the matrix cores: value
+ * scales that a row sees should be within a factor of 2^90 of each other (a page of
+ * zeros counts as 2^-31). */
 i8l_status int8_cache_attention(const i8l_kv_cache *cache, const i8l_sequences *seqs,
                                 const uint16_t *q, int64_t q_token_stride,
                                 int64_t q_head_stride, int64_t q_heads, int64_t rows,
