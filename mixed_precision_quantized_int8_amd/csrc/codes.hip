@@ -83,29 +83,33 @@ __global__ __launch_bounds__(kCrThreads) void codes_row_kernel(CodesArgs a) {
   }
 }
 
-// ---- more rows: 128 x 64 tiles, split along k ----------------------------------------
-// Eight waves, one 32 x 32 block each (v_mfma_i32_32x32x32_i8); steps of 128 bytes of
+// ---- more rows: 128 x 64 or 128 x 128 tiles, split along k ----------------------------
+// Eight waves, NB blocks of 32 x 32 each (v_mfma_i32_32x32x32_i8); steps of 128 bytes of
 // k through a ring of four LDS slots, filled by direct loads three steps ahead.  With
 // more than one split the int32 sums go to part [split][M][N] and codes_join_kernel
 // adds them: 4 bytes times the number of splits per output, against the 64 MB that
-// 256 x 256 tiles need to fill the chip.
-constexpr int kCtM = 128, kCtN = 64, kCtK = 128, kCtRing = 4, kCtThreads = 512;
-constexpr int kCtA = kCtM * kCtK, kCtB = kCtN * kCtK;
+// 256 x 256 tiles need to fill the chip.  Bound by latency while k is short (257 x 1040
+// x 300 8.4 us, nine steps), then by what a compute unit can have on its way of rows that
+// several tiles share (4096 x 14336 x 256: 32 us, 235 MB through L2, 7 TB/s).
+constexpr int kCtM = 128, kCtK = 128, kCtRing = 4, kCtThreads = 512;
+constexpr int kCtA = kCtM * kCtK;
 
 __device__ __forceinline__ int ct_swz(int row) { return ((row >> 1) & 3) | (((row >> 4) & 1) << 2); }
 
+template <int NB>
 __global__ __launch_bounds__(kCtThreads, 1) void codes_tile_kernel(CodesArgs a) {
+  constexpr int kCtN = 64 * NB, kCtB = kCtN * kCtK;
   __shared__ __attribute__((aligned(1024))) int8_t smem[kCtRing * (kCtA + kCtB)];
   int8_t* const sA = smem;
   int8_t* const sB = smem + kCtRing * kCtA;
   const int M = a.M, N = a.N, K = a.K;
   const int tiles_n = (N + kCtN - 1) / kCtN, tiles = tiles_n * ((M + kCtM - 1) / kCtM);
   // Workgroup b runs on XCD b % 8.  Narrow products give each XCD a run of
-  // neighbouring tiles, whose rows of codes its L2 then reads once (4096 x 14336 x 256:
-  // 42 -> 36 us); wide ones, tile by tile, a share of the weight (1024 x 4096 x 1024:
-  // 16.5 against 18.9).
+  // neighbouring tiles, whose rows of codes its L2 then reads once (4096 x 14336 x 256
+  // in tiles of 64: 42 -> 36 us); wide ones, tile by tile, a share of the weight (1024 x
+  // 4096 x 1024: 16.5 against 18.9).
   const int items = tiles * a.n_split;
-  const int item = tiles_n > 8 ? (int)blockIdx.x : blockIdx.x % 8 * ((items + 7) / 8) + blockIdx.x / 8;
+  const int item = tiles_n * kCtN > 512 ? (int)blockIdx.x : blockIdx.x % 8 * ((items + 7) / 8) + blockIdx.x / 8;
   if (item >= items) return;
   const int tile = item % tiles, split = item / tiles;
   const int m0 = tile / tiles_n * kCtM, n0 = tile % tiles_n * kCtN;
@@ -113,21 +117,24 @@ __global__ __launch_bounds__(kCtThreads, 1) void codes_tile_kernel(CodesArgs a) 
   const int s0 = (int)((int64_t)split * nk / a.n_split), s1 = (int)((int64_t)(split + 1) * nk / a.n_split);
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int l32 = lane & 31, lh = lane >> 5;
-  const int wm = (wave & 3) * 32, wn = (wave >> 2) * 32;
+  const int wm = (wave & 3) * 32, wn = (wave >> 2) * 32 * NB;
 
-  // loads of a step: A rows 16 wave .. +15 (two of 8), B rows 8 wave .. +7, 16 bytes
-  // a lane; rows past the end repeat the last
-  const int8_t* ga[2];
-  int ka[2];
+  // loads of a step: A rows 16 wave .. +15 (two of 8), B rows 8 NB wave .. +8 NB - 1,
+  // 16 bytes a lane; rows past the end repeat the last
+  const int8_t *ga[2], *gb[NB];
+  int ka[2], kb[NB];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int row = (wave * 2 + i) * 8 + (lane >> 3);
     ka[i] = ((lane & 7) ^ ct_swz(row)) * 16;
     ga[i] = a.Xq + (size_t)min(m0 + row, M - 1) * K;
   }
-  const int rb = wave * 8 + (lane >> 3);
-  const int kb = ((lane & 7) ^ ct_swz(rb)) * 16;
-  const int8_t* gb = a.Wq + (size_t)min(n0 + rb, N - 1) * K;
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int row = (wave * NB + i) * 8 + (lane >> 3);
+    kb[i] = ((lane & 7) ^ ct_swz(row)) * 16;
+    gb[i] = a.Wq + (size_t)min(n0 + row, N - 1) * K;
+  }
 #define I8L_CT_LDS(p) ((__attribute__((address_space(3))) void*)(p))
   auto load_step = [&](int s) {   // past the end: the last step again, into a free slot
     const int slot = s % kCtRing, k = min(s, s1 - 1) * kCtK;
@@ -137,40 +144,72 @@ __global__ __launch_bounds__(kCtThreads, 1) void codes_tile_kernel(CodesArgs a) 
       __builtin_amdgcn_global_load_lds((const void*)g,
                                        I8L_CT_LDS(&sA[slot * kCtA + (wave * 2 + i) * 1024]), 16, 0, 0);
     }
-    const int8_t* g = k + kb < K ? gb + k + kb : g_codes_zero;
-    __builtin_amdgcn_global_load_lds((const void*)g, I8L_CT_LDS(&sB[slot * kCtB + wave * 1024]), 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int8_t* g = k + kb[i] < K ? gb[i] + k + kb[i] : g_codes_zero;
+      __builtin_amdgcn_global_load_lds((const void*)g,
+                                       I8L_CT_LDS(&sB[slot * kCtB + (wave * NB + i) * 1024]), 16, 0, 0);
+    }
   };
-  v16i_c acc = v16i_c{};
+  // the epilogue's scales, of this lane's rows m0 + wm + 8 (r / 4) + 4 lh + r % 4 and
+  // features, on their way before the first step
+  float sx[16], sw[NB], bias[NB];
+  if (a.n_split == 1) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      sx[r] = a.sx[min(m0 + wm + 8 * (r >> 2) + 4 * lh + (r & 3), M - 1)];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int n = min(n0 + wn + 32 * j + l32, N - 1);
+      sw[j] = a.sw[n];
+      bias[j] = a.bias ? h2f(a.bias[n]) : 0.0f;
+    }
+  }
+  v16i_c acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) acc[j] = v16i_c{};
   load_step(s0);
   load_step(s0 + 1);
   load_step(s0 + 2);
   const int ra = wm + l32, rw = wn + l32;
   for (int s = s0; s < s1; ++s) {
-    // vmcnt(6): step s has landed, the six loads of steps s + 1 and s + 2 may fly;
+    // vmcnt: step s has landed, the 2 (2 + NB) loads of steps s + 1 and s + 2 may fly;
     // lgkmcnt(0): step s - 1 has been read from the slot that step s + 3 goes to
-    __builtin_amdgcn_s_waitcnt(6 | (0x7 << 4));
+    __builtin_amdgcn_s_waitcnt((4 + 2 * NB) | (0x7 << 4));
     asm volatile("s_barrier" ::: "memory");   // for every wave; step s - 1 is consumed
     load_step(s + 3);
     const int slot = s % kCtRing;
+    v4i fa[4], fb[4][NB];   // all of the step's operands on their way before the first product
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int c = 2 * q + lh;
-      const v4i fa = *reinterpret_cast<const v4i*>(&sA[slot * kCtA + ra * kCtK + ((c ^ ct_swz(ra)) << 4)]);
-      const v4i fb = *reinterpret_cast<const v4i*>(&sB[slot * kCtB + rw * kCtK + ((c ^ ct_swz(rw)) << 4)]);
-      acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa, fb, acc, 0, 0, 0);
+      fa[q] = *reinterpret_cast<const v4i*>(&sA[slot * kCtA + ra * kCtK + ((c ^ ct_swz(ra)) << 4)]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int row = rw + 32 * j;
+        fb[q][j] = *reinterpret_cast<const v4i*>(&sB[slot * kCtB + row * kCtK + ((c ^ ct_swz(row)) << 4)]);
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[q], fb[q][j], acc[j], 0, 0, 0);
   }
   // (the loads still on their way go to LDS, which must outlive them)
   __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xf << 8));   // vmcnt(0)
-  const int n = n0 + wn + l32;
-  if (n >= N) return;
-  const float sw = a.sw[n], bias = a.bias ? h2f(a.bias[n]) : 0.0f;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int m = m0 + wm + 8 * (r >> 2) + 4 * lh + (r & 3);
-    if (m >= M) continue;
-    if (a.n_split > 1) a.part[((size_t)split * M + m) * N + n] = acc[r];
-    else a.Y[(size_t)m * N + n] = codes_out(acc[r], a.sx[m], sw, bias);
+  for (int j = 0; j < NB; ++j) {
+    const int n = n0 + wn + 32 * j + l32;
+    if (n >= N) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int m = m0 + wm + 8 * (r >> 2) + 4 * lh + (r & 3);
+      if (m >= M) continue;
+      if (a.n_split > 1) a.part[((size_t)split * M + m) * N + n] = acc[j][r];
+      else a.Y[(size_t)m * N + n] = codes_out(acc[j][r], sx[r], sw[j], bias[j]);
+    }
   }
 }
 
@@ -204,7 +243,7 @@ __global__ __launch_bounds__(256) void codes_join_kernel(CodesArgs a) {
 }
 
 CodesPlan codes_plan(int M, int N, int K) {
-  CodesPlan p{CodesPlan::kGemm, 1, 0};
+  CodesPlan p{CodesPlan::kGemm, 1, 0, 0};
   if (M <= kStreamMaxM) {
     // 16 features a workgroup until 64 of them fill the chip as well: 1 x 4096 x 8192
     // 8.3 against 10.8 us, x 16384 14.1 against 13.0; 64 x 4096 x 4096 12.6 against
@@ -214,12 +253,18 @@ CodesPlan codes_plan(int M, int N, int K) {
   }
   // 128 x 64 tiles while 256 x 256 ones would leave three quarters of the chip idle,
   // or half of it over a short k: 256 x 4096 x 4096 18.8 against 24.2 us (skinny
-  // tiles), x 16384 39.4 against 30.1; 1024 x 4096 x 2048 19.4 against 42.4 (256 x 256),
-  // x 4096 35.5 against 46.7, 1024 x 14336 x 4096 106 against 82.
+  // tiles), x 16384 39.4 against 30.1; 1024 x 4096 x 2048 20.4 against 42.4 (256 x 256),
+  // x 4096 29.3 against 46.7, 1024 x 14336 x 4096 no gain.
   const int64_t wide = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
   if (wide < 64 || (M > kSkinnyMaxM && wide < 128 && K <= 8192)) {
     p.kind = CodesPlan::kTiles;
-    const int64_t tiles = (int64_t)((M + kCtM - 1) / kCtM) * ((N + kCtN - 1) / kCtN);
+    // 128 features a tile where 64 would need more workgroups than compute units (1024 x
+    // 4096 x 4096 37.4 -> 29.3 us), or over a long k that is split anyway (4096 x 14336 x
+    // 256 37.0 -> 34.2, 300 x 14336 x 2048 31.9 -> 27.2); else they start later and leave
+    // units idle (256 x 4096 x 1024 14.1 against 15.8, x 14336 x 1024 16.6 against 21.1).
+    const int64_t rows = (M + kCtM - 1) / kCtM, narrow = rows * ((N + 63) / 64);
+    p.tile_n = narrow > 256 || (narrow >= 96 && K > 8192) ? 128 : 64;
+    const int64_t tiles = rows * ((N + p.tile_n - 1) / p.tile_n);
     // a workgroup a compute unit; at least four steps of k a split, and none where k is
     // so short that the join would take longer (16 steps)
     const int nk = (K + kCtK - 1) / kCtK;
@@ -250,9 +295,10 @@ hipError_t launch_codes(CodesArgs a, const CodesPlan& p, const int32_t* zeros, h
   }
   if (p.kind == CodesPlan::kTiles) {
     a.n_split = a.part ? p.n_split : 1;
-    const int tiles = ((a.M + kCtM - 1) / kCtM) * ((a.N + kCtN - 1) / kCtN);
-    hipLaunchKernelGGL(codes_tile_kernel, dim3((tiles * a.n_split + 7) / 8 * 8), dim3(kCtThreads), 0,
-                       stream, a);
+    const int tiles = ((a.M + kCtM - 1) / kCtM) * ((a.N + p.tile_n - 1) / p.tile_n);
+    const dim3 grid((tiles * a.n_split + 7) / 8 * 8), block(kCtThreads);
+    if (p.tile_n == 64) hipLaunchKernelGGL(codes_tile_kernel<1>, grid, block, 0, stream, a);
+    else hipLaunchKernelGGL(codes_tile_kernel<2>, grid, block, 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_split == 1) return e;
     const size_t quads = ((size_t)a.M * a.N + 3) / 4;

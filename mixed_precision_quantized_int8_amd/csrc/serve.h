@@ -40,6 +40,7 @@ struct CodesPlan {
   enum Kind { kStream, kRows, kTiles, kSkinny, kGemm } kind;
   int n_split;
   size_t workspace;       // bytes of partial sums
+  int tile_n;             // kTiles: features of a tile, 64 or 128
 };
 CodesPlan codes_plan(int M, int N, int K);
 hipError_t launch_codes(CodesArgs a, const CodesPlan& p, const int32_t* zeros, hipStream_t stream);

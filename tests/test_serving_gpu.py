@@ -164,6 +164,8 @@ CODES = [(1, 16, 1), (1, 4096, 1000), (8, 4096, 16384), (16, 1024, 33), (17, 272
          (700, 1040, 77)]
 # the layer's own kernels on codes: streaming, skinny tiles, 256 x 256 tiles whole and split
 CODES += [(32, 1040, 5000), (3, 528, 8500), (80, 272, 16400), (200, 1040, 16500), (300, 80, 16640), (512, 2048, 33000)]
+# 128 features a tile: many tiles, one of 32 features at the end, k split by 5
+CODES += [(2300, 272, 1000), (1100, 1040, 2900), (300, 8208, 2050)]
 
 
 @pytest.mark.parametrize("M,K,N", CODES)
