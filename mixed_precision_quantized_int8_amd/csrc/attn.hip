@@ -87,8 +87,8 @@ __device__ __forceinline__ void say_empty(const AttnArgs& a, int b, int h, int r
 // LDS at the end.  The matrix cores run 16 columns for however many rows there are;
 // converting the codes is the larger part of the vector work, a few times below the
 // memory's rate.  One sequence of 131072 tokens, 112 heads of 128: 3.76 GB in
-// 615 us, 6.1 TB/s; 64 sequences of 2 - 8 thousand, 32 heads on 8: 684 MB in 156 us,
-// 4.4 TB/s (a large copy reaches 5.15); 100 tokens, 16 heads of 64: 5.8 us, latency.
+// 615 us, 6.1 TB/s; 64 sequences of 2 - 8 thousand, 32 heads on 8: 684 MB in 153 us,
+// 4.5 TB/s (a large copy reaches 5.15); 100 tokens, 16 heads of 64: 5.8 us, latency.
 // A third workgroup a compute unit (168 registers) was slower: 167 and 743 us; two
 // blocks of 16 rows a wave too (32 rows, 64 heads, 65536 keys: 321 against 303 us).
 //
