@@ -297,13 +297,15 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
   }
 
   // keys of the incomplete page, 16 bits each; values past the length are
-  // whatever the slot held before and are cleared
+  // whatever the slot held before and are cleared.  So are infinities and NaNs, which
+  // a hidden key's weight of 0 would spread over all rows: where there is one, each lane
+  // adds those that its query sees.
   auto tail_tile = [&](int t0) {
     const int slot = a.s.slots ? a.s.slots[b] : b;
     const bool ok = slot >= 0 && slot < a.c.n_slots;
     const size_t f = ((size_t)(ok ? slot : 0) * H + h) * page_sz;
     const int tk = t0 + 16 * (i16 >> 2), tv = t0 + 16 * grp;
-    const bool in_k = tk >= coded && tk < coded + P, in_v = tv >= coded && tv < coded + P;
+    const bool in_k = tk >= coded && tk < coded + P, in_v = ok && tv >= coded && tv < coded + P;
     v4f s[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -321,21 +323,55 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
     }
     float base = 0.0f;
     if (ALIBI) base = slope * (float)(tv - pos);
-    soften(s, sc, base, 1.0f, t0, false, max(lo, coded), hi, ok);
+    const int from = max(lo, coded);
+    soften(s, sc, base, 1.0f, t0, false, from, hi, ok);
+    v4u v[2][ND];
+    uint32_t odd = 0;
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-      const v4u p = weights(s, st);
       const int k0 = tv + 8 * st, nv = in_v ? sq.len - k0 : 0;   // valid keys of these eight
       const uint16_t* vp = a.c.vt + f + (size_t)i16 * P + (in_v ? k0 - coded : 0);
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
-        v4u v = {0, 0, 0, 0};
-        if (16 * d < D) v = *reinterpret_cast<const v4u*>(vp + (size_t)16 * d * P);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          v[u] &= (2 * u < nv ? 0xffffu : 0u) | (2 * u + 1 < nv ? 0xffff0000u : 0u);
-        o[d] = mfma16<BF>(v, p, o[d]);
+        v[st][d] = v4u{0, 0, 0, 0};
+        if (16 * d < D) v[st][d] = *reinterpret_cast<const v4u*>(vp + (size_t)16 * d * P);
       }
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          v[st][d][u] &= (2 * u < nv ? 0xffffu : 0u) | (2 * u + 1 < nv ? 0xffff0000u : 0u);
+          odd |= odd_halves<BF>(v[st][d][u]);
+        }
+    }
+    if (__any(odd)) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t x = v[st][d][u];
+            asm volatile("" : "+v"(x));   // (found again here, not kept from above)
+            v[st][d][u] = clear_halves(x, odd_halves<BF>(x));
+          }
+      for (int k = max(t0, from); k < min(t0 + kAdTile, hi); ++k) {
+        const uint16_t* vp = a.c.vt + f + (4 * grp << ps) + k - coded;   // of this lane's outputs
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          asm volatile("" : "+v"(vp));   // (an address at a time)
+          if (16 * d < D)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] += odd_value<BF>(vp[e << ps]);
+          vp += 16 << ps;
+        }
+      }
+    }
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const v4u p = weights(s, st);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] = mfma16<BF>(v[st][d], p, o[d]);
     }
   };
 
@@ -431,6 +467,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Att
   __shared__ __attribute__((aligned(1024))) uint8_t s_kv[2 * kBuf];
   // per 16 keys: score factor, log2 of the value scale, 1 / it
   __shared__ __attribute__((aligned(16))) float s_mul[2][4], s_base[2][4], s_inv[2][4];
+  __shared__ uint32_t s_odd[2];   // a tile of the incomplete page holds infinities or NaNs
 
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -762,6 +799,9 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Att
     last_outputs(n_coded - 1, 1);
   }
   // ---- the keys of the incomplete page, 16 bits each, a tile at a time -------------
+  // Infinities and NaNs among the values are cleared, since a hidden key's weight of 0
+  // would spread them over all rows; each row then adds those that it sees.
+  if (t < 2) s_odd[t] = 0;
   for (int j = 0; j < n_tail; ++j) {
     const int t0 = coded + j * kApTile, r0 = j * kApTile;
     const int slot = a.s.slots ? a.s.slots[b] : b;
@@ -776,16 +816,22 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Att
         x = *reinterpret_cast<const v4u*>(a.c.kt + f + (size_t)(r0 + key) * D + piece * 8);
       *reinterpret_cast<v4u*>(s_kv + key * DP * 2 + ((piece ^ (key & KMASK)) << 4)) = x;
     }
+    uint32_t odd = 0;
     for (int c = t; c < DP * kApTile / 8; c += NT) {   // past the length: zeros
       const int d = c >> 3, piece = c & 7, nv = n - piece * 8;
       v4u x = {0, 0, 0, 0};
       if (nv > 0 && d < D)
         x = *reinterpret_cast<const v4u*>(a.c.vt + f + (size_t)d * P + r0 + piece * 8);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q) {
         x[q] &= (2 * q < nv ? 0xffffu : 0u) | (2 * q + 1 < nv ? 0xffff0000u : 0u);
+        const uint32_t bad = odd_halves<BF>(x[q]);
+        odd |= bad;
+        x[q] = clear_halves(x[q], bad);
+      }
       *reinterpret_cast<v4u*>(s_kv + kKeys + d * kApTile * 2 + ((piece ^ ((d >> 1) & 7)) << 4)) = x;
     }
+    if (odd) s_odd[j] = 1;   // (at most two tiles)
     if (t < 4) store_meta(0, ok, 1.0f, 1.0f);
     lds_sync();
     load_meta(0);
@@ -803,6 +849,19 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Att
       for (int e = 0; e < 8; ++e) weigh(k, e);
       total(k);
       last_outputs(0, k);
+    }
+    if (s_odd[j] != 0) {   // uniform
+      for (int key = max(t0, lo); key < min(t0 + kApTile, hi); ++key) {
+        const uint16_t* vp = a.c.vt + f + (4 * hf << ps) + key - coded;   // of this lane's outputs
+#pragma unroll
+        for (int q = 0; q < 4 * ND; ++q) {
+          asm volatile("" : "+v"(vp));   // (an address at a time)
+          if (8 * q + 4 * hf < D)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[q >> 2][4 * (q & 3) + e] += odd_value<BF>(vp[e << ps]);
+          vp += 8 << ps;
+        }
+      }
     }
   }
 
@@ -862,11 +921,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   float l = 0.0f;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // elements lane + 64 u
   for (int s0 = 0; s0 < a.n_split; s0 += 64) {
-    float f = 0.0f;
+    float f = 0.0f, ls = 0.0f;
     if (s0 + lane < a.n_split) {
       f = __builtin_amdgcn_exp2f(ml[2 * (s0 + lane)] - ms);
-      l = __builtin_fmaf(ml[2 * (s0 + lane) + 1], f, l);
+      ls = ml[2 * (s0 + lane) + 1];
+      l = __builtin_fmaf(ls, f, l);
     }
+    // an empty split has no output; one whose weight underflows counts, by an infinity in it
+    const uint64_t some = __ballot(ls != 0.0f);
     const int n = min(64, a.n_split - s0);
     for (int j = 0; j < n; j += 8) {
       float fj[8], x[8][4];
@@ -874,8 +936,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
       for (int e = 0; e < 8; ++e) {
         fj[e] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), j + e));
 #pragma unroll
-        for (int u = 0; u < 4; ++u)   // (an empty split has no output)
-          x[e][u] = fj[e] != 0.0f && 64 * u < D && lane + 64 * u < D
+        for (int u = 0; u < 4; ++u)
+          x[e][u] = (some >> (j + e) & 1) && 64 * u < D && lane + 64 * u < D
                         ? po[(size_t)(s0 + j + e) * D + lane + 64 * u]
                         : 0.0f;
       }

@@ -33,6 +33,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {   // one v_cvt_pk
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
 }
 
+// Infinities and NaNs among two packed values: the top bit of each such half (the
+// exponent's ones carry into it), those halves cleared, and one value alone (0 if finite).
+template <bool BF>
+__device__ __forceinline__ uint32_t odd_halves(uint32_t x) {
+  return ((x & 0x7fff7fffu) + (BF ? 0x00800080u : 0x04000400u)) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t clear_halves(uint32_t x, uint32_t odd) {
+  return x & ~(odd | (odd - (odd >> 15)));
+}
+template <bool BF>
+__device__ __forceinline__ float odd_value(uint16_t b) {
+  return odd_halves<BF>(b) ? to_f32<BF>(b) : 0.0f;
+}
+
 // D = A . B + C over 32 contraction elements, 16 x 16 (A row / B column =
 // lane & 15, elements 8 * (lane >> 4) .. +7; D column = lane & 15, rows
 // 4 * (lane >> 4) .. +3).

@@ -1,0 +1,164 @@
+"""The serving operators at the edges of their ranges, on the GPU against the CPU
+oracle."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import serving_oracle as O  # noqa: E402
+from test_serving_gpu import TYPES, U, World, gen, same, say  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib(i8l):
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    return i8l
+
+
+def contents(cache):
+    return {n: getattr(cache, n).clone()
+            for n in ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail")}
+
+
+# ---- non-finite values in the incomplete page ---------------------------------------
+
+HIDDEN = [
+    # len, queries, H, G, D, P, window, distance of the bad token from the end
+    (40, 30, 1, 1, 64, 64, 0, 3),           # 16 rows a workgroup
+    (40, 9, 2, 3, 48, 64, 0, 3),
+    (104, 30, 1, 1, 80, 64, 5, 20),          # behind the window of the last queries
+    (100, 1, 2, 1, 64, 64, 5, 20),           # a single query, the bad token behind its window
+    (227, 100, 1, 1, 128, 128, 0, 60),       # a tail of two tiles, the bad token in the first
+    (227, 100, 1, 1, 256, 128, 9, 10),       # ... in the second
+    (3000, 12, 1, 1, 64, 128, 0, 5),         # keys split over workgroups
+    (2410, 300, 8, 4, 64, 128, 0, 7),        # runs: 256 rows a workgroup
+    (1400, 1200, 8, 8, 80, 128, 40, 70),     # ... the bad token behind the window
+    (1120, 300, 6, 3, 256, 64, 0, 9),        # runs: 128 rows a workgroup
+    (7100, 40, 8, 2, 128, 128, 0, 11),       # ... split
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,m,H,G,D,P,window,back", HIDDEN)
+def test_attention_tail_hides_non_finite_values(lib, n, m, H, G, D, P, window, back, dtype):
+    """An infinity or a NaN in a token of the incomplete page shows in the queries that
+    see the token, in its dimension and sign, and in no other."""
+    say("hidden values", n, m, H, G, D, P, window, back, dtype)
+    w = World(lib, [n], H, D, P, dtype, seed=n + m + D, fill=False)
+    bad = n - 1 - back
+    assert bad >= n // P * P
+    clean = w.v[0].clone()
+    w.v[0][bad, :, 1], w.v[0][bad, :, 2], w.v[0][bad, 0, 3] = math.inf, -math.inf, math.nan
+    w.write([0], [n])
+    q = torch.randn((m, H * G, D), generator=gen(n)).to(w.dt)
+    y = lib.cache_attention(q.cuda(), w.cache, w.table, w.lengths, cu=w.cu([m]), slots=w.slots,
+                            window=window).cpu().double()
+    pos = torch.arange(n - m, n)
+    sees = pos >= bad
+    if window:
+        sees &= pos - bad < window
+    w.v[0] = clean
+    (k, v, s), = w.stored()
+    o, tol = O.attention(q, k, v, D ** -0.5, window, None, s, U[w.dt])
+    good = (y - o).abs() <= tol
+    assert bool(good[~sees].all())
+    assert bool(good[sees][:, :, 4:].all()) and bool(good[sees][:, :, 0].all())
+    assert bool((y[sees][:, :, 1] == math.inf).all()) and bool((y[sees][:, :, 2] == -math.inf).all())
+    assert bool(y[sees][:, :G, 3].isnan().all()) and bool(good[sees][:, G:, 3].all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,m,H,G,D,P,window,back", HIDDEN)
+def test_attention_tail_hides_non_finite_keys(lib, n, m, H, G, D, P, window, back, dtype):
+    """A key of NaNs in the incomplete page: the queries that see it are NaN, the others
+    are as without it."""
+    say("hidden keys", n, m, H, G, D, P, window, back, dtype)
+    w = World(lib, [n], H, D, P, dtype, seed=n + m + D, fill=False)
+    bad = n - 1 - back
+    clean = w.k[0].clone()
+    w.k[0][bad] = math.nan
+    w.write([0], [n])
+    q = torch.randn((m, H * G, D), generator=gen(n)).to(w.dt)
+    y = lib.cache_attention(q.cuda(), w.cache, w.table, w.lengths, cu=w.cu([m]), slots=w.slots,
+                            window=window).cpu().double()
+    pos = torch.arange(n - m, n)
+    sees = pos >= bad
+    if window:
+        sees &= pos - bad < window
+    w.k[0] = clean
+    (k, v, s), = w.stored()
+    o, tol = O.attention(q, k, v, D ** -0.5, window, None, s, U[w.dt])
+    assert bool(((y - o).abs() <= tol)[~sees].all())
+    assert bool(y[sees].isnan().all())
+
+
+def test_attention_infinity_far_below_the_maximum(lib):
+    """An infinite value whose weight is below fp32's range, in a split of its own or not:
+    the output is not finite (its weight is positive)."""
+    for n in (300, 5000):
+        w = World(lib, [n], 1, 64, 128, "fp16", seed=n, fill=False)
+        w.v[0][n - 1, 0, 3] = math.inf
+        w.k[0][:100] = 30.0
+        w.k[0][n - 1] = -30.0
+        w.write([0], [n])
+        q = torch.ones((1, 1, 64)).half().cuda()
+        y = lib.cache_attention(q, w.cache, w.table, w.lengths, slots=w.slots).cpu()[0, 0]
+        assert not bool(y[3].isfinite())
+        assert bool(y[:3].isfinite().all()) and bool(y[4:].isfinite().all())
+
+
+# ---- pages and slots outside the cache --------------------------------------------------
+
+
+def test_cache_write_outside_the_cache_touches_nothing_else(lib):
+    """With page numbers and slots outside the cache every other byte keeps its value: all
+    six tensors."""
+    w = World(lib, [48, 20], 1, 64, 16, "fp16", seed=4)
+    before = contents(w.cache)
+    table = w.table.clone()
+    table[0, :3] = torch.tensor([-5, w.cache.n_pages, 2 ** 31 - 1])
+    slots = torch.tensor([-1, 99], dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((68, 1, 64), generator=gen(s)).half() for s in (5, 6))
+    lib.cache_write(w.cache, k.cuda(), v.cuda(), table, w.lengths, cu=w.cu([48, 20]), slots=slots)
+    p, st = int(table[1, 0]), O.Store(16)
+    for name, x, tr in (("k", k, False), ("v", v, True)):
+        c, s = st.page(x[48:64, 0])
+        want = before[name + "_codes"]
+        want[p, 0] = (c.t() if tr else c).to(want.device)
+        same(getattr(w.cache, name + "_codes"), want)
+        want = before[name + "_scale"]
+        want[p, 0] = s
+        same(getattr(w.cache, name + "_scale"), want)
+        same(getattr(w.cache, name + "_tail"), before[name + "_tail"])
+
+
+def test_slots_outside_the_cache_hide_the_tail(lib):
+    """Attention masks the tokens of a slot outside the cache, in both kernels; cache_read
+    gives zeros for them."""
+    lens, H, G, D, P = [1000, 20], 8, 2, 64, 64
+    w = World(lib, lens, H, D, P, "fp16", seed=41)
+    for slots in ([-1, 99], [2 ** 31 - 1, -2 ** 31]):
+        slots = torch.tensor(slots, dtype=torch.int32, device="cuda")
+        for m in (1, 200, 600):
+            Q = [m, min(m, 20)]
+            q = [torch.randn((c, H * G, D), generator=gen(c)).half() for c in Q]
+            y = lib.cache_attention(torch.cat(q).cuda(), w.cache, w.table, w.lengths, cu=w.cu(Q),
+                                    slots=slots).cpu().double()
+            assert bool((y[m:] == 0).all())
+            k, v, s = w.stored()[0]
+            held = 1000 // P * P
+            j = min(m, held - (1000 - m))          # rows whose token is in a complete page
+            if j > 0:
+                o, tol = O.attention(q[0][:j], k[:1000 - m + j], v[:1000 - m + j], D ** -0.5,
+                                     page_scale=s[:1000 - m + j])
+                assert bool(((y[:j] - o).abs() <= tol).all())
+            o, tol = O.attention(q[0][-1:], k[:held], v[:held], D ** -0.5, page_scale=s[:held])
+            assert bool(((y[m - 1:m] - o).abs() <= tol).all())
+        k, v = lib.cache_read(w.cache, w.table, w.lengths, w.cu(lens), 1020, slots=slots)
+        for got, i in ((k, 0), (v, 1)):
+            same(got[:held], w.stored()[0][i][:held].half())
+            assert bool((got[held:] == 0).all())
