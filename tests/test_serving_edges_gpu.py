@@ -111,6 +111,69 @@ def test_attention_infinity_far_below_the_maximum(lib):
         assert bool(y[:3].isfinite().all()) and bool(y[4:].isfinite().all())
 
 
+# ---- the norm over bf16's range -----------------------------------------------------
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+@pytest.mark.parametrize("K", [256, 1040, 4096, 14336, 40000, 65552])
+def test_rmsnorm_quant_over_the_range_of_bf16(lib, K, eps):
+    """Rows whose squares fp32 cannot hold, at both ends: the scale is absmax / rms there
+    as anywhere, for every launch shape and with h in place of either operand."""
+    say("rmsnorm_quant over bf16's range", K, eps)
+    E = [126, 120, 100, 70, 64, 60, 0, -40, -60, -66, -70, -75, -80, -90]
+    g = gen(K)
+    base = (torch.rand((len(E), K), generator=g) * 1.5 - 0.75).bfloat16()
+    base[:, 3] = 1.0
+    two = torch.tensor([2.0 ** e for e in E])[:, None]
+    X = (base.float() * two).bfloat16()        # (powers of two: exact)
+    X[0, 5] = 1.0                              # one small value in a row of huge ones
+    R = (X.float() * 0.25).bfloat16()
+    W = (1 + 0.1 * torch.rand(K, generator=g)).bfloat16()
+    for r, w in ((None, None), (R, W)):
+        x, rr = X.cuda(), None if r is None else r.cuda()
+        q0, s0, h0 = O.rmsnorm_quant(X, w, r, eps)
+        q, s, h = lib.rmsnorm_quant(x, None if w is None else w.cuda(), residual=rr, eps=eps)
+        same(q, q0)
+        same(h, h0)
+        # the tolerance of test_rmsnorm_quant, and fp32's last place where the scale is
+        # below its normal numbers
+        assert bool(((s.cpu().double() - s0).abs() <= 1e-5 * s0 + 2.0 ** -149).all())
+        if r is not None:
+            q2, s2, h2 = lib.rmsnorm_quant(x, w.cuda(), residual=rr, eps=eps, residual_out=rr)
+            same(q2, q0)
+            same(h2, h0)
+            same(s2, s)
+
+
+def test_rmsnorm_quant_small_weights_and_large_eps(lib):
+    """Rows of subnormals lifted by their weight, an eps near fp32's largest: the scale is
+    a / sqrt(mean h^2 + eps)."""
+    X = torch.rand((3, 512), generator=gen(1)) * 0.5
+    X[:, 1] = 1.0
+    X = (X * torch.tensor([2.0 ** -120, 2.0 ** 63, 2.0 ** 80])[:, None]).bfloat16()
+    W = torch.full((512,), 2.0 ** 40).bfloat16()
+    W[7] = 2.0 ** 20
+    for w, eps in ((W, 0.0), (W, 1e-30), (None, 3e38), (W * 2.0 ** -60, 1e38)):
+        q0, s0, _ = O.rmsnorm_quant(X, w, None, eps)
+        q, s, _ = lib.rmsnorm_quant(X.cuda(), None if w is None else w.cuda(), eps=eps)
+        same(q, q0)
+        s = s.cpu().double()
+        assert bool(((s - s0).abs() <= 1e-5 * s0 + 2.0 ** -149).all()), (eps, s, s0)
+
+
+def test_rmsnorm_quant_non_finite_rows_of_bf16(lib):
+    """An infinity or a NaN in h still shows in the scale of its row, beside rows of huge
+    finite values."""
+    X = (torch.rand((5, 1040), generator=gen(2)) + 0.5).bfloat16() * 2.0 ** 100
+    X[1, 700], X[3, 2] = math.inf, math.nan
+    R = X.clone()
+    R[4, 9] = X[4, 9] = 3.0e38                 # their sum overflows
+    _, s, h = lib.rmsnorm_quant(X.cuda(), residual=R.cuda())
+    s = s.cpu()
+    assert s.isnan().tolist() == [False, True, False, True, True]
+    assert bool((s[[0, 2]] > 0).all()) and bool(s[[0, 2]].isfinite().all())
+
+
 # ---- pages and slots outside the cache --------------------------------------------------
 
 
