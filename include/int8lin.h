@@ -362,8 +362,8 @@ typedef struct {
 
 /* The sequences of a call (device arrays).  Entries are clamped to what the
  * tensors hold: a page or slot outside the cache is neither read nor written
- * (its tokens are skipped; attention masks them), a length past
- * max_pages * page_size ends there. */
+ * (its tokens are skipped; attention masks them), tokens past
+ * max_pages * page_size are skipped and masked too, but count in the positions. */
 typedef struct {
   const int32_t *page_table;  /* [n][max_pages]: page of tokens i * page_size .. */
   const int32_t *lengths;     /* [n]: tokens of each sequence, this call's included */

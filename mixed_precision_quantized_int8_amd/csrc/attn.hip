@@ -34,19 +34,20 @@ constexpr float kLeastScale = 0x1p-100f;
 
 struct Rows {          // a sequence's part of the call
   int64_t c0;          // first row in q and out
-  int n, len;          // queries, tokens held
-  int first_pos;       // position of its first query
+  int n, len;          // queries, tokens held (those that the page table has a place for)
+  int first_pos;       // position of its first query; counts the tokens past the table
 };
 __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int b) {
   Rows r;
-  const int64_t most = (int64_t)a.s.max_pages << a.c.ps;
-  r.len = (int)min((int64_t)max(a.s.lengths[b], 0), most);
+  // (lengths end at 2^30, past any page table, so that positions stay in 32 bits)
+  const int len = min(max(a.s.lengths[b], 0), 1 << 30);
   int64_t c0 = a.s.cu ? a.s.cu[b] : b, c1 = a.s.cu ? a.s.cu[b + 1] : b + 1;
   c0 = min(max(c0, (int64_t)0), a.rows);
   c1 = min(max(c1, c0), a.rows);
   r.c0 = c0;
   r.n = (int)min(c1 - c0, (int64_t)a.max_q);   // (none past max_q is written)
-  r.first_pos = (int)max((int64_t)r.len - (c1 - c0), -((int64_t)1 << 30));
+  r.len = min(len, a.s.max_pages << a.c.ps);
+  r.first_pos = (int)max(len - (c1 - c0), -((int64_t)1 << 30));
   return r;
 }
 

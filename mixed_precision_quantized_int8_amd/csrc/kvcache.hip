@@ -35,21 +35,22 @@ struct CacheRows {
 };
 
 // A sequence's part of a call, from device data that is clamped to what the
-// tensors hold: rows c0 .. c0 + n - 1 are its last n tokens.
+// tensors hold: row c0 + i is token p0 + i, up to token len - 1, the last that the
+// page table has a place for (the rows after it are skipped).
 struct Span {
   int64_t c0;
-  int n, len;
+  int p0, len;
 };
 __device__ __forceinline__ Span seq_span(const Sequences& s, int b, int ps, int64_t rows) {
   Span r;
-  const int64_t most = (int64_t)s.max_pages << ps;
-  r.len = (int)min((int64_t)max(s.lengths[b], 0), most);
+  const int most = s.max_pages << ps, len = max(s.lengths[b], 0);
   int64_t c0 = s.cu ? s.cu[b] : b, c1 = s.cu ? s.cu[b + 1] : b + 1;
   c0 = min(max(c0, (int64_t)0), rows);
   c1 = min(max(c1, c0), rows);
-  if (c1 - c0 > r.len) c0 = c1 - r.len;   // more rows than tokens: the last ones
+  if (c1 - c0 > len) c0 = c1 - len;   // more rows than tokens: the last ones
   r.c0 = c0;
-  r.n = (int)(c1 - c0);
+  r.p0 = len - (int)(c1 - c0);
+  r.len = min(len, most);
   return r;
 }
 
@@ -96,8 +97,9 @@ __device__ __forceinline__ void write_page(const Cache& c, const Sequences& s, c
                                            int b, int h, int task, uint8_t* lds, uint32_t* red) {
   const int ps = c.ps, P = 1 << ps, D = c.D, D8 = D >> 3, t = threadIdx.x;
   const Span sp = seq_span(s, b, ps, x.rows);
-  if (sp.n == 0) return;
-  const int p0 = sp.len - sp.n, g0 = p0 >> ps, gl = (sp.len - 1) >> ps;
+  const int p0 = sp.p0;
+  if (p0 >= sp.len) return;
+  const int g0 = p0 >> ps, gl = (sp.len - 1) >> ps;
   const int g = g0 + task;
   if (g > gl) return;
   const int full = sp.len >> ps;   // complete pages

@@ -244,8 +244,8 @@ def cache_write(cache, k, v, page_table, lengths, cu=None, slots=None, max_new=N
     k, v [rows][heads][head_dim] of the cache's type (strided views are fine:
     multiples of 8 elements).  Sequence i's rows are cu[i] .. cu[i+1] - 1 (int32
     [n+1]; None: row i alone) and become its last tokens: ``lengths`` (int32 [n])
-    counts them in.  ``page_table`` int32 [n][pages] names its pages, ``slots``
-    int32 [n] its tail slot (None: slot i).  ``max_new``: at least the rows of any
+    counts them in.  ``page_table`` int32 [n][pages] names its pages (tokens past them
+    are skipped), ``slots`` int32 [n] its tail slot (None: slot i).  ``max_new``: at least the rows of any
     one sequence (None: all rows; a closer bound launches fewer workgroups).
     """
     s = _sequences(cache, page_table, lengths, cu, slots)

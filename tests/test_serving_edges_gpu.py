@@ -174,6 +174,54 @@ def test_rmsnorm_quant_non_finite_rows_of_bf16(lib):
     assert bool((s[[0, 2]] > 0).all()) and bool(s[[0, 2]].isfinite().all())
 
 
+# ---- sequences that outgrow their page table ------------------------------------------
+
+
+def test_cache_write_past_the_page_table(lib):
+    """Tokens past max_pages * page_size are skipped: complete pages and tails keep their
+    bits, whatever the slot holds by then; the tokens before the end are written."""
+    P, H, D = 16, 2, 64
+    w = World(lib, [32, 30, 20], H, D, P, "fp16", seed=31)
+    w.cache.k_tail[int(w.slots[0])] = 3.0          # sequence 0 has no tail: its slot is anyone's
+    w.cache.v_tail[int(w.slots[0])] = 3.0
+    before = contents(w.cache)
+    k = torch.randn((3, H, D), generator=gen(1)).half().cuda()
+    lens = torch.tensor([33, 40, 1 << 30], dtype=torch.int32, device="cuda")
+    lib.cache_write(w.cache, k, k, w.table, lens, slots=w.slots)
+    for name, t in contents(w.cache).items():
+        same(t, before[name])
+    # six new tokens of sequence 1, two of which its table holds
+    new_k, new_v = (torch.randn((6, H, D), generator=gen(s)).half() for s in (2, 3))
+    table = w.table[1:2].contiguous()
+    lib.cache_write(w.cache, new_k.cuda(), new_v.cuda(), table,
+                    torch.tensor([36], dtype=torch.int32, device="cuda"), cu=w.cu([6]),
+                    slots=w.slots[1:2].contiguous())
+    w.k[1], w.v[1] = torch.cat([w.k[1], new_k[:2]]), torch.cat([w.v[1], new_v[:2]])
+    w.lens = [32, 32, 20]
+    w.check_content()
+
+
+@pytest.mark.parametrize("m,H,G", [(1, 2, 2), (3, 2, 2), (300, 8, 4)])
+def test_attention_past_the_page_table(lib, m, H, G):
+    """The positions of queries count the tokens past the table, which are out of sight."""
+    P, D, held, n, window = 64, 64, 1024, 1027, 300
+    w = World(lib, [held], H, D, P, "fp16", seed=32)
+    q = torch.randn((m, H * G, D), generator=gen(m)).half()
+    y = lib.cache_attention(q.cuda(), w.cache, w.table,
+                            torch.tensor([n], dtype=torch.int32, device="cuda"), cu=w.cu([m]),
+                            slots=w.slots, window=window).cpu().double()
+    (k, v, s), = w.stored()
+    for j in range(m):
+        last = min(n - m + j, held - 1)
+        first = max(0, n - m + j + 1 - window)
+        if j % 37 and 2 < j < m - 4:
+            continue
+        # the last query of a sequence that ends at `last`, over the keys from `first` on
+        o, tol = O.attention(q[j:j + 1], k[first:last + 1], v[first:last + 1], D ** -0.5,
+                             page_scale=s[first:last + 1])
+        assert bool(((y[j:j + 1] - o).abs() <= tol).all()), j
+
+
 # ---- pages and slots outside the cache --------------------------------------------------
 
 
