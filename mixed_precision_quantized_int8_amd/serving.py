@@ -155,7 +155,9 @@ class KVCache:
       k_tail [n_slots][heads][P][head_dim], v_tail [n_slots][heads][head_dim][P]
           fp16 or bf16: the tokens of each sequence's last, incomplete page
 
-    P is 16, 32, 64 or 128; head_dim a multiple of 16 up to 256.
+    P is 16, 32, 64 or 128; head_dim a multiple of 16 up to 256.  The cache holds the
+    tensors' addresses: its attributes do not change (a larger pool is a new KVCache over
+    new tensors), and the tensors must not be resized or given other storage.
     """
 
     __slots__ = ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "heads",
@@ -167,17 +169,22 @@ class KVCache:
             raise ValueError("k_codes must be a tensor [n_pages][heads][page_size][head_dim]")
         n, H, P, D = k_codes.shape
         slots, dev, dt = k_tail.shape[0], k_codes.device, k_tail.dtype
-        self._struct = _binding.KVCacheStruct(
+        struct = _binding.KVCacheStruct(
             _dense(k_codes, torch.int8, (n, H, P, D), None, "k_codes"),
             _dense(v_codes, torch.int8, (n, H, D, P), dev, "v_codes"),
             _dense(k_scale, torch.float32, (n, H), dev, "k_scale"),
             _dense(v_scale, torch.float32, (n, H), dev, "v_scale"),
             _dense(k_tail, dt, (slots, H, P, D), dev, "k_tail"),
             _dense(v_tail, dt, (slots, H, D, P), dev, "v_tail"), n, slots, H, D, P, code)
-        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
-        self.k_tail, self.v_tail = k_tail, v_tail
-        self.heads, self.page_size, self.head_dim = H, P, D
-        self.dtype, self.device = dt, dev
+        for put, x in zip(_CACHE_FIELDS, (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, H, P, D,
+                                          dt, dev, struct)):
+            put(self, x)
+
+    def __setattr__(self, name, x):
+        raise AttributeError(f"{name}: a KVCache does not change; make a new one over new tensors")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name}: a KVCache does not change")
 
     @property
     def n_pages(self):
@@ -186,6 +193,10 @@ class KVCache:
     @property
     def n_slots(self):
         return self._struct.n_slots
+
+
+# what the constructor writes an unchanging cache's attributes with
+_CACHE_FIELDS = [KVCache.__dict__[name].__set__ for name in KVCache.__slots__]
 
 
 def new_cache(n_pages, n_slots, heads, head_dim, page_size=64, dtype=torch.float16,

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import serving_oracle as O  # noqa: E402
-from test_serving_gpu import TYPES, U, World, gen, same, say  # noqa: E402
+from test_serving_gpu import TYPES, U, World, gen, run_attention, same, say  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -273,3 +273,21 @@ def test_slots_outside_the_cache_hide_the_tail(lib):
         for got, i in ((k, 0), (v, 1)):
             same(got[:held], w.stored()[0][i][:held].half())
             assert bool((got[held:] == 0).all())
+
+
+# ---- a cache and its tensors ----------------------------------------------------------
+
+
+def test_a_larger_pool_is_a_new_cache(lib):
+    """A cache's tensors stay as they were made; the pages of one move into a larger one
+    by copying the tensors."""
+    w = World(lib, [40, 33], 2, 64, 16, "fp16", seed=61)
+    with pytest.raises(AttributeError, match="new one"):
+        w.cache.k_codes = torch.empty_like(w.cache.k_codes)
+    old = w.cache
+    big = lib.new_cache(old.n_pages + 5, old.n_slots, 2, 64, 16, w.dt, "cuda:0")
+    for name, t in contents(old).items():
+        getattr(big, name)[:t.shape[0]].copy_(t)
+    w.cache = big
+    w.check_content()
+    run_attention(w, 2, [1, 1])
