@@ -60,13 +60,14 @@ __device__ __forceinline__ float xsum16(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
-// Partial results of a split launch: (m, l) of every row and split, then its
-// unnormalised output (not written where l is 0 and m -infinity).
+// Partial results of a split launch: (m, l) of every row and split, filled up to 16
+// bytes, then its unnormalised output (not written where l is 0 and m -infinity).
+__host__ __device__ __forceinline__ size_t part_head(size_t count) { return (2 * count + 3) / 4 * 4; }
 __device__ __forceinline__ size_t part_at(const AttnArgs& a, int b, int h, int row, int split) {
   return (((size_t)b * a.c.H + h) * ((size_t)a.G * a.max_q) + row) * a.n_split + split;
 }
 __device__ __forceinline__ float* part_out(const AttnArgs& a, size_t at) {
-  return a.part + 2 * ((size_t)a.s.B * a.c.H * a.G * a.max_q * a.n_split) + at * a.c.D;
+  return a.part + part_head((size_t)a.s.B * a.c.H * a.G * a.max_q * a.n_split) + at * a.c.D;
 }
 __device__ __forceinline__ void say_empty(const AttnArgs& a, int b, int h, int row, int split) {
   const size_t at = part_at(a, b, h, row, split);
@@ -1041,7 +1042,8 @@ hipError_t launch_typed(const AttnArgs& a, const Plan& p, hipStream_t stream) {
 
 size_t attention_partials(int B, int H, int G, int D, int max_q, int max_len, int window) {
   const Plan p = plan(B, H, G, D, max_q, max_len, window);
-  return p.n_split == 1 ? 0 : (size_t)B * H * G * max_q * p.n_split * (size_t)(D + 2);
+  const size_t count = (size_t)B * H * G * max_q * p.n_split;
+  return p.n_split == 1 ? 0 : part_head(count) + count * D;
 }
 
 hipError_t launch_attention(AttnArgs a, hipStream_t stream) {

@@ -1,4 +1,6 @@
 """Serving operators, edges that need no GPU."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -14,3 +16,16 @@ def test_a_cache_does_not_change_its_tensors(i8l):
             setattr(c, name, torch.zeros(1))
         with pytest.raises(AttributeError):
             delattr(c, name)
+
+
+def test_partial_results_are_aligned(i8l):
+    """Attention's workspace holds (maximum, sum) of every row and split, filled up to 16
+    bytes, then their outputs, which are written 16 bytes at a time."""
+    from test_serving_abi import cache_struct
+
+    for heads, n, max_len, splits in ((1, 1, 700, 3), (5, 3, 700, 3), (1, 1, 500, 2)):
+        for D in (16, 64, 256):
+            c = cache_struct(heads=heads, head_dim=D)
+            count = n * heads * splits
+            need = i8l.lib().i8l_attention_workspace_bytes(ctypes.byref(c), n, heads, 1, max_len, 0)
+            assert need == 4 * ((2 * count + 3) // 4 * 4 + count * D)

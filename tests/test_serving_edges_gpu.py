@@ -291,3 +291,18 @@ def test_a_larger_pool_is_a_new_cache(lib):
     w.cache = big
     w.check_content()
     run_attention(w, 2, [1, 1])
+
+
+# ---- partial results of split keys --------------------------------------------------------
+
+
+@pytest.mark.parametrize("lens,Q,H,G,D,alibi", [
+    ([700], 1, 1, 1, 64, False), ([700, 650, 600], 1, 5, 1, 80, True), ([700], 1, 1, 1, 256, False),
+    ([2000, 30], 1, 1, 7, 176, False), ([900], 3, 1, 1, 128, False), ([2800], 33, 3, 1, 256, True)])
+def test_attention_odd_numbers_of_partial_results(lib, lens, Q, H, G, D, alibi):
+    """Rows times splits odd, and heads of 256 with split keys."""
+    for dtype in TYPES:
+        say("odd partial results", lens, Q, H, G, D, alibi, dtype)
+        w = World(lib, lens, H, D, 32, dtype, seed=sum(lens) + D)
+        assert lib.attention_workspace_bytes(w.cache, len(lens), H * G, Q, max(lens)) > 0
+        run_attention(w, G, [Q] * len(lens), 0, alibi)
