@@ -2,7 +2,8 @@
 codes, the product of codes that are already there, a key/value cache held in 8
 bits, and attention over it.  Marshalling only, as in the package's __init__:
 every step runs in the HIP kernels of libint8lin.so (include/int8lin.h states
-the formulas).
+the formulas).  For inference: there are no gradients, and a tensor that requires
+one is refused where torch records them.
 
     Xq, sx, h = rmsnorm_quant(X, weight, residual=r)   # norm of X + r as row codes
     Y = linear_codes(Xq, sx, Wq, sw)                   # their product with a weight
@@ -39,6 +40,15 @@ def _stream(device):
     if _raw_stream is not None:
         return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _inference(*tensors):
+    """Refuses tensors that would need a gradient: these operators have none, and a result
+    without one would end the graph unnoticed."""
+    for t in tensors:
+        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
+            raise RuntimeError("the serving operators have no gradients, but an argument requires "
+                               "one: call them under torch.no_grad() or detach it")
 
 
 def _dense(t, dtype, shape, device, name):
@@ -103,6 +113,7 @@ def rmsnorm_quant(X, weight=None, residual=None, eps=1e-5, Xq=None, sx=None, res
     ``sx`` and ``residual_out`` (which may be ``residual`` or ``X``) receive the
     results if given.
     """
+    _inference(X, weight, residual)
     code = _half_type(X, "X", 2)
     (M, K), dev, dt = X.shape, X.device, X.dtype
     x = _dense(X, dt, (M, K), None, "X")
@@ -127,6 +138,7 @@ def linear_codes(Xq, sx, Wq, sw, bias=None, out=None, workspace=None):
     (uint8) takes the partial sums of shapes that are split along K (for more than
     64 rows); None allocates what the shape needs.
     """
+    _inference(sx, sw, bias)
     if not isinstance(Xq, torch.Tensor) or not isinstance(Wq, torch.Tensor):
         raise TypeError("Xq and Wq must be torch.Tensors")
     if Xq.dim() != 2 or Wq.dim() != 2:
@@ -259,6 +271,7 @@ def cache_write(cache, k, v, page_table, lengths, cu=None, slots=None, max_new=N
     are skipped), ``slots`` int32 [n] its tail slot (None: slot i).  ``max_new``: at least the rows of any
     one sequence (None: all rows; a closer bound launches fewer workgroups).
     """
+    _inference(k, v)
     s = _sequences(cache, page_table, lengths, cu, slots)
     kp, kt, kh = _rows(k, cache, cache.heads, "k")
     vp, vt, vh = _rows(v, cache, cache.heads, "v")
@@ -314,6 +327,7 @@ def cache_attention(q, cache, page_table, lengths, cu=None, slots=None, max_q=No
     holds) the longest sequence; sequences, cu and slots as for ``cache_write``.
     ``workspace`` (uint8, ``attention_workspace_bytes``): None allocates it.
     """
+    _inference(q, alibi)
     s = _sequences(cache, page_table, lengths, cu, slots)
     qp, qt, qh = _rows(q, cache, None, "q")
     rows, heads, D = q.shape

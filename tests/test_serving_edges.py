@@ -29,3 +29,26 @@ def test_partial_results_are_aligned(i8l):
             count = n * heads * splits
             need = i8l.lib().i8l_attention_workspace_bytes(ctypes.byref(c), n, heads, 1, max_len, 0)
             assert need == 4 * ((2 * count + 3) // 4 * 4 + count * D)
+
+
+def test_tensors_that_require_a_gradient_are_refused(i8l):
+    """No result without a gradient where one is expected; under no_grad() the call goes on
+    (here to the next refusal, of tensors that are not on a GPU)."""
+    X, W = torch.zeros((2, 64)).half(), torch.zeros(64).half()
+    G = torch.zeros((2, 64)).half().requires_grad_()
+    f = torch.ones(2, requires_grad=True)
+    kv = torch.zeros((1, 1, 16)).half().requires_grad_()
+    refused = [lambda: i8l.rmsnorm_quant(G, W), lambda: i8l.rmsnorm_quant(X, W, residual=G),
+               lambda: i8l.rmsnorm_quant(X, torch.nn.Parameter(W)),
+               lambda: i8l.linear_codes(X, f, X, W), lambda: i8l.linear_codes(X, W, X, f),
+               lambda: i8l.linear_codes(X, W, X, W, bias=G), lambda: i8l.cache_write(None, kv, X, X, X),
+               lambda: i8l.cache_write(None, X, kv, X, X),
+               lambda: i8l.cache_attention(kv, None, X, X),
+               lambda: i8l.cache_attention(X, None, X, X, alibi=f)]
+    for call in refused:
+        with pytest.raises(RuntimeError, match="no gradients"):
+            call()
+    with torch.no_grad():
+        for call in refused:
+            with pytest.raises((TypeError, ValueError)):
+                call()
