@@ -306,7 +306,9 @@ typedef enum { I8L_FP16 = 0, I8L_BF16 = 1 } i8l_dtype;
  *   Xq = clamp(round_half_away(g * fl32(127 / a)), -127, 127)   (0 where a is 0),
  *   sx = a / sqrt(mean_k h^2 + eps),
  * so that Xq * sx / 127 is the norm's value: the operands of int8_linear_codes.
- * The factor 1 / rms is common to the row and enters the scale alone.
+ * The factor 1 / rms is common to the row and enters the scale alone.  No outlier
+ * columns are set apart: a column c times as large as the others leaves those
+ * 127 / c steps (int8_linear on 16-bit rows has them).
  *   X         [M][K]  dtype, 16-byte aligned
  *   residual  [M][K]  dtype, or NULL
  *   weight    [K]     dtype, or NULL (ones)
