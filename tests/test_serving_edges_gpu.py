@@ -275,6 +275,56 @@ def test_slots_outside_the_cache_hide_the_tail(lib):
             assert bool((got[held:] == 0).all())
 
 
+# ---- workspaces that the caller gives, or does not ---------------------------------------
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 1000), (8, 4096, 16384), (65, 2064, 257), (300, 8208, 1000),
+                                   (300, 8208, 2000), (520, 8208, 1900), (200, 1040, 16500),
+                                   (512, 2048, 33000)])
+def test_linear_codes_workspaces(lib, M, K, N):
+    """The caller's workspace, one too large, and none at all (nothing is then split along
+    k) give the same bits; one too small is refused."""
+    from mixed_precision_quantized_int8_amd._binding import check
+
+    say("linear_codes, workspaces", M, K, N)
+    g = gen(M + N)
+    Xq = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8).cuda()
+    Wq = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8).cuda()
+    sx, sw = torch.rand(M, generator=g).cuda(), (torch.rand(N, generator=g) * 0.1).cuda()
+    y0, mag = O.linear_codes(Xq.cpu(), sx.cpu(), Wq.cpu(), sw.cpu())
+    want = lib.linear_codes(Xq, sx, Wq, sw)
+    # the tolerance of test_linear_codes
+    assert bool(((want.cpu().double() - y0).abs()
+                 <= 2.0 ** -11 * y0.abs() + 2.0 ** -22 * mag + 2.0 ** -25).all())
+    need = lib.lib().i8l_codes_workspace_bytes(M, K, N)
+    for extra in (0, 4096):
+        ws = torch.full((need + extra,), 0x7f, dtype=torch.uint8, device="cuda")
+        same(lib.linear_codes(Xq, sx, Wq, sw, workspace=ws), want)
+    out = torch.full_like(want, math.nan)
+    check(lib.lib().int8_linear_codes(Xq.data_ptr(), sx.data_ptr(), M, K, Wq.data_ptr(), sw.data_ptr(),
+                                      N, None, out.data_ptr(), None, 0,
+                                      torch.cuda.current_stream().cuda_stream))
+    same(out, want)
+    if need > 16:
+        with pytest.raises(lib.Int8LinError, match="workspace"):
+            lib.linear_codes(Xq, sx, Wq, sw, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_attention_workspaces(lib):
+    """The caller's workspace holds the partial results; a call without one allocates it."""
+    w = World(lib, [3000, 700], 2, 64, 64, "fp16", seed=51)
+    q = torch.randn((2, 4, 64), generator=gen(7)).half().cuda()
+    args = (q, w.cache, w.table, w.lengths)
+    want = lib.cache_attention(*args, slots=w.slots, max_len=3000)
+    need = lib.attention_workspace_bytes(w.cache, 2, 4, 1, 3000)
+    assert need > 0
+    for extra in (0, 1 << 16):
+        ws = torch.full((need + extra,), 0x7f, dtype=torch.uint8, device="cuda")
+        same(lib.cache_attention(*args, slots=w.slots, max_len=3000, workspace=ws), want)
+    with pytest.raises(lib.Int8LinError, match="workspace"):
+        lib.cache_attention(*args, slots=w.slots, max_len=3000, workspace=ws[:need - 16])
+
+
 # ---- a cache and its tensors ----------------------------------------------------------
 
 
