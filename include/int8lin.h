@@ -408,7 +408,9 @@ size_t i8l_attention_workspace_bytes(const i8l_kv_cache *cache, int64_t n, int64
  * the tokens max(0, i - window + 1) .. i (window 0: all up to i):
  *   out = softmax_t(scale * q . k_t - alibi[head] * (i - t)) . v_t,
  * with the cache's 8-bit values (16-bit in the tail).  Query head h reads kv
- * head h / (q_heads / heads).  A query that sees no token gives 0.
+ * head h / (q_heads / heads).  A query that sees no token gives 0.  Infinities and
+ * NaNs show in the queries that see them (a complete page that holds one reads as NaN
+ * as a whole; in the incomplete page they stay in their token and dimension).
  *   q      [rows][q_heads][head_dim] dtype; element (t, h, d) at
  *          t * token_stride + h * head_stride + d (multiples of 8)
  *   alibi  fp32 [q_heads] slopes, or NULL

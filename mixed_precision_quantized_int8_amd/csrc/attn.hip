@@ -10,8 +10,9 @@
 //   s'_j = s_j + ln vs_j,   m = max_j s'_j,   w_j = exp(s'_j - m) <= 1,
 //   o = sum_j w_j c^v_j / sum_j w_j / vs_j,
 // so the product on the matrix cores runs on the codes themselves, and the
-// rounding of w_j to 16 bits is relative to the largest contribution.  Codes
-// are exact in fp16 and bf16; m and the sums are fp32.  The tokens of the incomplete
+// rounding of w_j to 16 bits is relative to the largest contribution (it takes the
+// error against 64 bits from 2.1e-4 to 2.4e-4 - 2.9e-4 in fp16, from 1.7e-3 to 2.0e-3
+// in bf16).  Codes are exact in fp16 and bf16; m and the sums are fp32.  The tokens of the incomplete
 // page have 16-bit values and no scale; every kernel takes them last, since weights
 // relative to them would lose bits where the codes' scales are small.
 #include <algorithm>
@@ -89,8 +90,9 @@ __device__ __forceinline__ void say_empty(const AttnArgs& a, int b, int h, int r
 // LDS at the end.  The matrix cores run 16 columns for however many rows there are;
 // converting the codes is the larger part of the vector work, a few times below the
 // memory's rate.  One sequence of 131072 tokens, 112 heads of 128: 3.76 GB in
-// 615 us, 6.1 TB/s; 64 sequences of 2 - 8 thousand, 32 heads on 8: 684 MB in 153 us,
-// 4.5 TB/s (a large copy reaches 5.15); 100 tokens, 16 heads of 64: 5.8 us, latency.
+// 617 to 641 us, 5.9 - 6.1 TB/s; 64 sequences of 2 - 8 thousand, 32 heads on 8: 684 MB in
+// 153 us, 4.5 TB/s (a large copy reaches 5.15); both in bf16 156 and 645 us; 100 tokens,
+// 16 heads of 64: 5.4 us, latency.  (Passes in a captured graph, the join included.)
 // A third workgroup a compute unit (168 registers) was slower: 167 and 743 us; two
 // blocks of 16 rows a wave too (32 rows, 64 heads, 65536 keys: 321 against 303 us).
 //
@@ -442,14 +444,17 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
 // The running maximum moves only when a score passes it by 8 (in log2): the
 // weights then stay below 2^8 and most tiles leave O alone.
 //
-// Bound by the matrix cores under the board's power limit: 4096 queries over 8192
-// tokens, 32 heads of 128 on 8, in 411 us, 1000 TFLOP/s (a large fp16 product reaches
-// 1080 on the same card); heads of 64 run at half that, on the exponentials.  What
+// Near what a large fp16 product reaches under the board's power limit (1080 TFLOP/s):
+// 4096 queries over 8192 tokens, 32 heads of 128 on 8, in 416 us, 990 TFLOP/s (bf16 405
+// us).  No unit is busy throughout: the matrix cores 47 % of the cycles, the vector unit
+// 58 %, LDS 38 %, in waves that issue in order, at 1.75 GHz.  Heads of 64 reach 775
+// TFLOP/s (the exponentials weigh twice as much), of 80 660 (padded to 128), of 256 855.
+// The instantiations for heads of 128 with four waves spill 4 to 7 registers.  What
 // carried it there: products and vector work in alternating slots (half_tile) with
 // staging that has no branches (638 -> 455 us; two groups of waves half a step
 // apart, with barriers, had been slower: 701); eight waves of 32 rows rather than
 // four of 64 (which left one wave a SIMD waiting: 752 us; with heads of 256 there is
-// no room for more, and the slots keep it at 760 TFLOP/s).
+// no room for more).
 constexpr int kApTile = 64;
 constexpr float kApSlack = 8.0f;
 

@@ -89,8 +89,9 @@ __global__ __launch_bounds__(kCrThreads) void codes_row_kernel(CodesArgs a) {
 // more than one split the int32 sums go to part [split][M][N] and codes_join_kernel
 // adds them: 4 bytes times the number of splits per output, against the 64 MB that
 // 256 x 256 tiles need to fill the chip.  Bound by latency while k is short (257 x 1040
-// x 300 8.4 us, nine steps), then by what a compute unit can have on its way of rows that
-// several tiles share (4096 x 14336 x 256: 32 us, 235 MB through L2, 7 TB/s).
+// x 300 8.4 us, nine steps), then by the wait for loads of rows that several tiles share, with
+// the eight waves in step (4096 x 14336 x 256: 32 us, 235 MB through L2, 7 TB/s; of the
+// busy cycles the matrix cores take 24 %, LDS 18 %, and 36 % of the waves' are waits).
 constexpr int kCtM = 128, kCtK = 128, kCtRing = 4, kCtThreads = 512;
 constexpr int kCtA = kCtM * kCtK;
 
@@ -262,6 +263,10 @@ CodesPlan codes_plan(int M, int N, int K) {
     // 4096 x 4096 37.4 -> 29.3 us), or over a long k that is split anyway (4096 x 14336 x
     // 256 37.0 -> 34.2, 300 x 14336 x 2048 31.9 -> 27.2); else they start later and leave
     // units idle (256 x 4096 x 1024 14.1 against 15.8, x 14336 x 1024 16.6 against 21.1).
+    // About the bound of 96: with 24 to 78 tiles of 64 they win or are level (300 x 8208 x
+    // 1664 19.2 against 21.5, x 14336 24.9 against 26.5, x 28672 40.9 against 41.0; 64 tiles
+    // of 512 x 28672 x 1024, the exception, 34.6 against 33.3), with 96 those of 128 (300 x
+    // 8208 x 2048 22.1 against 21.5, x 14336 30.9 against 26.7, x 28672 53.5 against 40.9).
     const int64_t rows = (M + kCtM - 1) / kCtM, narrow = rows * ((N + 63) / 64);
     p.tile_n = narrow > 256 || (narrow >= 96 && K > 8192) ? 128 : 64;
     const int64_t tiles = rows * ((N + p.tile_n - 1) / p.tile_n);

@@ -19,7 +19,7 @@
 //
 // Bound by HBM: 2 bytes in and 1 byte out per element written, 1 in and 2 out
 // per element read back.  24.8 thousand tokens of four sequences, 32 heads of 128,
-// bf16: 610 MB written in 134 us (4.6 TB/s), read back in 106 us (5.8 TB/s; a large
+// bf16: 610 MB written in 135 us (4.5 TB/s), read back in 109 us (5.6 TB/s; a large
 // copy reaches 5.15).  One token each of 16 sequences, 8 heads: 5.8 us, latency.
 #include "half.h"
 #include "serve.h"

@@ -11,11 +11,13 @@
 // The maximum is taken over the bits of |g|, whose order puts infinities and NaNs
 // last, so that either shows in sx.  A row whose a is below 2^-93 counts as zeros
 // (127 / a stays finite).  Rows of bf16 whose squares leave fp32's range are read
-// again and summed scaled by 2^-80 or 2^80: 88 us instead of 77 for 4096 x 14336 of them.
+// again and summed scaled by 2^-80 or 2^80: 88 us instead of 77 for 4096 x 14336 of them,
+// back to back.
 //
 // Bound by HBM: 2 + 2 bytes in, 2 + 1 bytes out per element.  4096 x 14336 fp16 with
-// a residual: 77 us, 5.3 TB/s (a large copy reaches 5.15); below a few hundred rows
-// by latency: 1 x 4096 2.7 us, 1 x 14336 4.4 us.
+// a residual: 70 us among the kernels of its case, 5.9 TB/s (a large copy reaches 5.15;
+// part of the rows is still in the last-level cache), 77 us back to back over five
+// inputs; below a few hundred rows by latency: 1 x 4096 2.7 us, 1 x 14336 4.4 us.
 #include "half.h"
 #include "serve.h"
 
@@ -194,8 +196,8 @@ static void launch_norm(const uint16_t* X, const uint16_t* R, const uint16_t* W,
 
 // Few chunks a thread: one row of 4096 takes 2.7 us with 512 threads, 3.1 with 256 and
 // 6.9 with 64, 4096 rows 25.3, 25.7 and 32.1; two chunks of 8192 elements 3.4 against
-// 4.1 us with four.  Up to 16384 elements four chunks cost nothing (14336: 77 us either
-// way) and 16384 x 4096 87 against 91 us.
+// 4.1 us with four.  Up to 16384 elements four chunks cost nothing (4096 x 14336: 77 us
+// back to back either way) and 16384 x 4096 87 against 91 us.
 hipError_t launch_rmsnorm_quant(const uint16_t* X, const uint16_t* R, const uint16_t* W, int M,
                                 int K, float eps, bool bf16, int8_t* Xq, float* sx, uint16_t* H,
                                 hipStream_t stream) {
