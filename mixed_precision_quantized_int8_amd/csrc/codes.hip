@@ -264,8 +264,8 @@ CodesPlan codes_plan(int M, int N, int K) {
     // 256 37.0 -> 34.2, 300 x 14336 x 2048 31.9 -> 27.2); else they start later and leave
     // units idle (256 x 4096 x 1024 14.1 against 15.8, x 14336 x 1024 16.6 against 21.1).
     // About the bound of 96: with 24 to 78 tiles of 64 they win or are level (300 x 8208 x
-    // 1664 19.2 against 21.5, x 14336 24.9 against 26.5, x 28672 40.9 against 41.0; 64 tiles
-    // of 512 x 28672 x 1024, the exception, 34.6 against 33.3), with 96 those of 128 (300 x
+    // 1664 19.2 against 21.5, x 14336 24.9 against 26.5, x 28672 40.9 against 41.0; 64 at a
+    // k of 28672 are the exception, 34 against 32 - 33), with 96 those of 128 (300 x
     // 8208 x 2048 22.1 against 21.5, x 14336 30.9 against 26.7, x 28672 53.5 against 40.9).
     const int64_t rows = (M + kCtM - 1) / kCtM, narrow = rows * ((N + 63) / 64);
     p.tile_n = narrow > 256 || (narrow >= 96 && K > 8192) ? 128 : 64;
