@@ -430,6 +430,145 @@ i8l_status int8_cache_attention(const i8l_kv_cache *cache, const i8l_sequences *
                                 const float *alibi, uint16_t *out, void *workspace,
                                 size_t workspace_bytes, void *stream);
 
+/* ---- Positions, and drafted tokens over the cache ------------------------------
+ * Rotary positions with the norm of each query and key head, on rows and on the way
+ * into the cache; attention for trees of drafted tokens behind the cached ones. */
+
+/* Rotary positions: pair i of a head at position p turns by the angle p * freqs[i]
+ * (formed in 64 bits), f = factor:
+ *   y_a = f (x_a cos - x_b sin),  y_b = f (x_a sin + x_b cos),
+ * pairs (a, b) = (i, i + pairs), or (2 i, 2 i + 1) if interleaved; elements from
+ * 2 * pairs on stay.  pairs 0 (freqs may be NULL): nothing turns. */
+typedef struct {
+  const float *freqs;    /* [pairs], device */
+  int32_t pairs;         /* 0 .. head_dim / 2 */
+  int32_t interleaved;   /* 0 or 1 */
+  float factor;          /* finite; of cos and sin (long contexts scale it) */
+} i8l_rotary;
+
+/* Heads to norm and turn.  Element (t, h, d) of x (of y) at t * token_stride +
+ * h * head_stride + d: strides in elements, multiples of 8; pointers 16-byte aligned. */
+typedef struct {
+  const uint16_t *x;
+  int64_t x_token_stride, x_head_stride;
+  uint16_t *y;             /* out; may be x, with x's strides */
+  int64_t y_token_stride, y_head_stride;
+  const uint16_t *weight;  /* [head_dim], 16-byte aligned, or NULL: no norm */
+  int32_t heads;           /* 1 .. 65536 */
+} i8l_heads;
+
+/* Norm and rotation of query heads and, in the same launch, of key heads:
+ *   n = x / sqrt(mean_d x^2 + eps) * weight   (x itself without a weight),
+ *   y = n turned to its row's position,
+ * all in fp32, rounded once.  A head of zeros gives zeros for any eps.
+ *   q, k       k may be NULL; both of `dtype` and head_dim (a multiple of 16, 16 .. 256)
+ *   positions  int32 [rows]
+ *   eps        >= 0 */
+i8l_status int8_rotate_heads(const i8l_heads *q, const i8l_heads *k, int32_t head_dim,
+                             int64_t rows, const int32_t *positions, const i8l_rotary *rotary,
+                             float eps, int dtype, void *stream);
+
+/* The gradient of int8_rotate_heads: dx of dy, and dweight (summed over rows and heads,
+ * in a fixed order) where there is a weight.  fp32 throughout, each result rounded once. */
+typedef struct {
+  const uint16_t *dy;
+  int64_t dy_token_stride, dy_head_stride;
+  const uint16_t *x;       /* the forward pass's input; unused (may be NULL) without weight */
+  int64_t x_token_stride, x_head_stride;
+  uint16_t *dx;            /* out; may be dy or x, with its strides */
+  int64_t dx_token_stride, dx_head_stride;
+  const uint16_t *weight;  /* as in the forward pass */
+  uint16_t *dweight;       /* [head_dim] out, with weight; 2-byte aligned */
+  int32_t heads;
+} i8l_heads_grad;
+
+/* Workspace bytes of int8_rotate_heads_backward where q or k has a weight (0: sizes
+ * that it refuses); without weights it needs none. */
+size_t i8l_rotate_heads_workspace_bytes(int64_t rows, int64_t q_heads, int32_t head_dim);
+
+/* rows == 0: dweight = 0.  workspace: 16-byte aligned. */
+i8l_status int8_rotate_heads_backward(const i8l_heads_grad *q, const i8l_heads_grad *k,
+                                      int32_t head_dim, int64_t rows, const int32_t *positions,
+                                      const i8l_rotary *rotary, float eps, int dtype,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* int8_cache_write with the keys' norm and rotation on the way and, in the same launch,
+ * the queries': bit for bit int8_rotate_heads on k (and q), then int8_cache_write.  The
+ * position of row j of a sequence with m rows is lengths - m + j.
+ *   rows      rows of the call: cu (and q) count in them
+ *   counts    int32 [n] or NULL: only the first counts[i] of the rows cu[i] ..
+ *             cu[i+1] - 1 (clamped to their number) are sequence i's
+ *   index     int32 [rows] or NULL: row r of the call is row index[r] of k and v
+ *             (clamped to them); q NULL then
+ *   kv_rows   rows of k and v (>= rows without an index)
+ *   max_new   at least the rows of any one sequence
+ *   q         NULL: no queries; q->y's rows outside the sequences are not written
+ *   k_weight  [head_dim] or NULL;  rotary NULL: nothing turns
+ * Everything else as for int8_cache_write. */
+i8l_status int8_cache_append(const i8l_kv_cache *cache, const i8l_sequences *seqs,
+                             const int32_t *counts, const int32_t *index, const uint16_t *k,
+                             int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v,
+                             int64_t v_token_stride, int64_t v_head_stride, int64_t kv_rows,
+                             int64_t rows, int64_t max_new, const i8l_heads *q,
+                             const uint16_t *k_weight, const i8l_rotary *rotary, float eps,
+                             void *stream);
+
+/* A tree of drafted tokens behind each sequence: draft j of a sequence (row cu[i] + j)
+ * follows its draft parents[cu[i] + j], or the cached text (-1; so does any entry that
+ * names no earlier draft).  At most I8L_MAX_DRAFTS a sequence.
+ *   lengths    int32 [n]: tokens cached, the drafts not among them
+ *   positions  int32 [rows] out: lengths + the draft's depth (0: it follows the text)
+ *   masks      uint64 [rows][words] out: bit b of word w is set if the draft is, or
+ *              descends from, draft 64 w + b
+ *   max_q      at least the drafts of any one sequence, at most 64 * words (rows past it
+ *              are not written; nor are rows that no sequence has)
+ * cu NULL: one draft a sequence. */
+#define I8L_MAX_DRAFTS 512
+i8l_status int8_tree_plan(const int32_t *parents, const int32_t *lengths, const int32_t *cu,
+                          int64_t n, int64_t rows, int64_t max_q, int32_t *positions,
+                          uint64_t *masks, int32_t words, void *stream);
+
+/* Attention of drafts over the cache, which does not hold them, and over each other: a
+ * draft's query at position p sees the cached tokens t with p - t < window (window 0:
+ * all), and the drafts of its sequence that its mask names, with the same window on
+ * their positions:
+ *   out = softmax(scale * q . k - alibi[head] * (p - position of the key)) . v.
+ * A query that sees nothing gives 0.
+ *   seqs       cu: the drafts' rows; lengths: tokens cached
+ *   q, k, v    [rows][q_heads or heads][head_dim] dtype, strided as for
+ *              int8_cache_attention; keys turned already
+ *   masks      uint64 [rows][words] (int8_tree_plan, or any)
+ *   positions  int32 [rows]; may be NULL without window and alibi
+ *   max_q      at least the drafts of any one sequence (those past it are neither seen
+ *              nor answered), at most 64 * words
+ *   workspace  i8l_attention_workspace_bytes(cache, n, q_heads, max_q, max_len, window)
+ * Everything else as for int8_cache_attention. */
+i8l_status int8_tree_attention(const i8l_kv_cache *cache, const i8l_sequences *seqs,
+                               const uint16_t *q, int64_t q_token_stride, int64_t q_head_stride,
+                               int64_t q_heads, const uint16_t *k, int64_t k_token_stride,
+                               int64_t k_head_stride, const uint16_t *v, int64_t v_token_stride,
+                               int64_t v_head_stride, int64_t rows, int64_t max_q,
+                               int64_t max_len, const uint64_t *masks, int32_t words,
+                               const int32_t *positions, float scale, int64_t window,
+                               const float *alibi, uint16_t *out, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* The path of drafts that the model's choices accept.  choices[r] is the token chosen to
+ * follow draft r; first[i] the token chosen to follow sequence i's cached text, or, first
+ * NULL, draft 0 of each sequence is that token already and accepted.  From an accepted
+ * draft the path goes on to the first of its children that is the chosen token.
+ *   tokens, choices  int64 [rows]; first int64 [n] or NULL
+ *   path         int32 [rows] out: from cu[i] on, the rows of sequence i's accepted drafts in
+ *                order, then -1 (int8_cache_append's index)
+ *   counts       int32 [n] out: their number (its counts)
+ *   new_lengths  int32 [n] out: lengths + counts
+ *   next         int64 [n] out: the token chosen to follow the path (-1: no draft, and no first)
+ * parents, lengths, cu and max_q (at most I8L_MAX_DRAFTS) as for int8_tree_plan. */
+i8l_status int8_tree_accept(const int32_t *parents, const int64_t *tokens, const int64_t *choices,
+                            const int64_t *first, const int32_t *lengths, const int32_t *cu,
+                            int64_t n, int64_t rows, int64_t max_q, int32_t *path,
+                            int32_t *counts, int32_t *new_lengths, int64_t *next, void *stream);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char *i8l_last_error(void);
 

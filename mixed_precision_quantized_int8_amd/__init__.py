@@ -8,8 +8,8 @@ libint8lin.so; torch supplies device memory and the current stream.
     Y = linear(X, Wq, sw, W, threshold=6.0)  # X fp16 [M][K] -> Y fp16 [M][N]
 
 Serving around the layer (serving.py: norm to codes, product of codes, an 8-bit
-key/value cache, attention over it) is reached from here too; decoder.py runs
-it together.
+key/value cache, attention over it) is reached from here too, as are rotary positions
+and drafted tokens over that cache (positions.py); decoder.py runs them together.
 """
 from __future__ import annotations
 
@@ -46,6 +46,15 @@ __all__ = [
     "cache_read",
     "cache_attention",
     "attention_workspace_bytes",
+    "Rotary",
+    "rotary",
+    "rotate_heads",
+    "rotate_heads_backward",
+    "rotate_heads_workspace_bytes",
+    "cache_append",
+    "tree_plan",
+    "tree_attention",
+    "tree_accept",
     "workspace_layout",
     "workspace_bytes",
     "workspace_views",
@@ -58,12 +67,23 @@ _SERVING = ("rmsnorm_quant", "linear_codes", "KVCache", "new_cache", "cache_writ
             "cache_attention", "attention_workspace_bytes")
 
 
+_POSITIONS = ("Rotary", "rotary", "rotate_heads", "rotate_heads_backward",
+              "rotate_heads_workspace_bytes", "cache_append", "tree_plan", "tree_attention",
+              "tree_accept")
+
+
 def __getattr__(name):
     if name in _SERVING:
         from . import serving
 
         for n in _SERVING:
             globals()[n] = getattr(serving, n)
+        return globals()[name]
+    if name in _POSITIONS:
+        from . import positions
+
+        for n in _POSITIONS:
+            globals()[n] = getattr(positions, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

@@ -47,6 +47,13 @@ EXPORTS = (
     "int8_cache_read",
     "i8l_attention_workspace_bytes",
     "int8_cache_attention",
+    "int8_rotate_heads",
+    "i8l_rotate_heads_workspace_bytes",
+    "int8_rotate_heads_backward",
+    "int8_cache_append",
+    "int8_tree_plan",
+    "int8_tree_attention",
+    "int8_tree_accept",
     "i8l_last_error",
     "i8l_build_info",
 )
@@ -104,6 +111,51 @@ class SequencesStruct(ctypes.Structure):
         ("slots", ctypes.c_void_p),
         ("n", ctypes.c_int32),
         ("max_pages", ctypes.c_int32),
+    ]
+
+
+class RotaryStruct(ctypes.Structure):
+    """i8l_rotary"""
+
+    _fields_ = [
+        ("freqs", ctypes.c_void_p),
+        ("pairs", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("factor", ctypes.c_float),
+    ]
+
+
+class HeadsStruct(ctypes.Structure):
+    """i8l_heads"""
+
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("x_token_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("y", ctypes.c_void_p),
+        ("y_token_stride", ctypes.c_int64),
+        ("y_head_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("heads", ctypes.c_int32),
+    ]
+
+
+class HeadsGradStruct(ctypes.Structure):
+    """i8l_heads_grad"""
+
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("dy_token_stride", ctypes.c_int64),
+        ("dy_head_stride", ctypes.c_int64),
+        ("x", ctypes.c_void_p),
+        ("x_token_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("dx", ctypes.c_void_p),
+        ("dx_token_stride", ctypes.c_int64),
+        ("dx_head_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p),
+        ("heads", ctypes.c_int32),
     ]
 
 
@@ -167,6 +219,25 @@ def lib() -> ctypes.CDLL:
     L.int8_cache_attention.argtypes = [cache, seqs, vp, i64, i64, i64, i64, i64, i64, f32, i64, vp,
                                        vp, vp, sz, vp]
     L.int8_cache_attention.restype = ctypes.c_int
+    rot, heads, grads = (ctypes.POINTER(t) for t in (RotaryStruct, HeadsStruct, HeadsGradStruct))
+    i32 = ctypes.c_int32
+    L.int8_rotate_heads.argtypes = [heads, heads, i32, i64, vp, rot, f32, ctypes.c_int, vp]
+    L.int8_rotate_heads.restype = ctypes.c_int
+    L.i8l_rotate_heads_workspace_bytes.argtypes = [i64, i64, i32]
+    L.i8l_rotate_heads_workspace_bytes.restype = sz
+    L.int8_rotate_heads_backward.argtypes = [grads, grads, i32, i64, vp, rot, f32, ctypes.c_int, vp,
+                                             sz, vp]
+    L.int8_rotate_heads_backward.restype = ctypes.c_int
+    L.int8_cache_append.argtypes = [cache, seqs, vp, vp, vp, i64, i64, vp, i64, i64, i64, i64, i64,
+                                    heads, vp, rot, f32, vp]
+    L.int8_cache_append.restype = ctypes.c_int
+    L.int8_tree_plan.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, i32, vp]
+    L.int8_tree_plan.restype = ctypes.c_int
+    L.int8_tree_attention.argtypes = [cache, seqs, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, i64,
+                                      i64, i64, vp, i32, vp, f32, i64, vp, vp, vp, sz, vp]
+    L.int8_tree_attention.restype = ctypes.c_int
+    L.int8_tree_accept.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp]
+    L.int8_tree_accept.restype = ctypes.c_int
     L.i8l_last_error.argtypes = []
     L.i8l_last_error.restype = ctypes.c_char_p
     L.i8l_build_info.argtypes = []

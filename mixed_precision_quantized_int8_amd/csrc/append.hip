@@ -1,0 +1,206 @@
+// Keys and values into the 8-bit cache with the keys' norm and rotation on the way, and
+// the queries' in the same launch: what rotate_heads and cache_write give one after the
+// other, bit for bit (the formulas are in rotary.h and kvcache.hip).
+//
+// A launch has three kinds of workgroups: a page of one head's keys, a page of one head's
+// values (kvcache.hip's way), and queries.  Keys are stored as they come, [token][D], so a
+// page of them is cut by rotary.h's units: 16 elements of one token a thread, both
+// elements of each pair among them, the norm's sum over a few neighbouring lanes.  The
+// turned keys are rounded to 16 bits, as the tail keeps them, before they are coded.
+#include "pages.h"
+#include "rotary.h"
+
+namespace i8l {
+
+// One page of one head of keys; task and tail as for write_page.
+template <bool BF, int LAYOUT, int BS, int NU>
+__device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, const CacheRows& x,
+                                            const HeadArgs& a, const uint16_t* k_w, int b, int h,
+                                            int task, float* row, uint32_t* red) {
+  constexpr int NT = 2 * NU;   // tokens a thread
+  const int ps = c.ps, P = 1 << ps, D = c.D, t = threadIdx.x, lane = t & 63;
+  const int lanes = lanes_of(D), j = t & (lanes - 1);
+  const Span sp = seq_span<true>(s, b, ps, x);
+  const int p0 = sp.p0;
+  if (p0 >= sp.len) return;
+  const int g0 = p0 >> ps, gl = (sp.len - 1) >> ps;
+  const int g = g0 + task;
+  if (g > gl) return;
+  const int full = sp.len >> ps;   // complete pages
+  const int slot = s.slots ? s.slots[b] : b;
+  const bool slot_ok = slot >= 0 && slot < c.n_slots;
+  uint16_t* tail = c.kt + ((size_t)(slot_ok ? slot : 0) * c.H + h) * P * D;
+  const uint16_t* rows = x.x[0] + h * x.hs[0];
+  const Runs at = runs_of<LAYOUT>(a.turn, j);
+  v4u w[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    w[r] = v4u{0, 0, 0, 0};
+    if (k_w && at.at[r] < D) w[r] = *reinterpret_cast<const v4u*>(k_w + at.at[r]);
+  }
+  // a token's 16 elements, normed and turned (every lane of the wave takes part)
+  auto turned = [&](v4u (&p)[2], int pos) {
+    float y[16];
+    unpack<BF>(p, y);
+    if (k_w) normed<BF>(y, w, rms_of<BF>(y, D, lanes, a.eps));
+    Angles<LAYOUT> angles;
+    angles.of(a.turn, j, pos, false);
+    turn<LAYOUT>(y, angles, a.turn, j, row, lane);
+    pack<BF>(y, p);
+  };
+  if (g < full) {
+    const int page = s.table[(size_t)b * s.max_pages + g];
+    const bool page_ok = page >= 0 && page < c.n_pages;
+    v4u p[NT][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int tok = (t + u * BS) / lanes, pos = (g << ps) + tok;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        p[u][r] = v4u{0, 0, 0, 0};
+        if (tok < P && at.at[r] < D) {
+          if (pos >= p0)
+            p[u][r] = *reinterpret_cast<const v4u*>(
+                rows + row_of<true>(x, sp.c0 + pos - p0) * x.ts[0] + at.at[r]);
+          else if (slot_ok)
+            p[u][r] = *reinterpret_cast<const v4u*>(tail + tok * D + at.at[r]);
+        }
+      }
+    }
+    // magnitudes of both types are in the order of their bits, infinities and NaNs last
+    u16x2 mag = {0, 0};
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int tok = (t + u * BS) / lanes, pos = (g << ps) + tok;
+      v4u q[2] = {p[u][0], p[u][1]};
+      turned(q, pos);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (pos >= p0) p[u][r] = q[r];   // (the tail's tokens are turned already)
+        if (tok < P && at.at[r] < D)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mag = __builtin_elementwise_max(mag, __builtin_bit_cast(u16x2, p[u][r][e] & 0x7fff7fffu));
+      }
+    }
+    uint32_t bits = wave_max_u32(mag[0] > mag[1] ? mag[0] : mag[1]);
+    if constexpr (BS > 64) {
+      if (lane == 0) red[t >> 6] = bits;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < BS / 64; ++i) bits = max(bits, red[i]);
+    }
+    const bool finite = bits < (BF ? 0x7f80u : 0x7c00u);
+    const float absmax = to_f32<BF>((uint16_t)bits);
+    const float top = absmax < kLeastMax ? 0.0f : absmax;
+    const float inv65 = (finite ? quant_scale(top) : 0.0f) * 65536.0f;
+    int8_t* out = c.kc + ((size_t)(page_ok ? page : 0) * c.H + h) * P * D;
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int tok = (t + u * BS) / lanes;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f = to_f32<BF>((uint16_t)(p[u][r][e >> 1] >> (16 * (e & 1))));
+          z[e] = code_bits(finite ? f : 0.0f, inv65);
+        }
+        uint2 k;
+        k.x = __builtin_amdgcn_perm(z[1], z[0], 0x0c0c0602u) | __builtin_amdgcn_perm(z[3], z[2], 0x06020c0cu);
+        k.y = __builtin_amdgcn_perm(z[5], z[4], 0x0c0c0602u) | __builtin_amdgcn_perm(z[7], z[6], 0x06020c0cu);
+        if (page_ok && tok < P && at.at[r] < D)
+          *reinterpret_cast<uint2*>(out + tok * D + at.at[r]) = k;
+      }
+    }
+    if (t == 0 && page_ok) c.ks[(size_t)page * c.H + h] = finite ? top / 127.0f : __builtin_nanf("");
+  }
+  if (task == 0 && gl >= full && slot_ok) {   // the last page stays incomplete
+    __syncthreads();   // the old tail has been read
+    const int lo = max(p0, full << ps);
+    for (int q0 = 0; q0 < (sp.len - lo) * lanes; q0 += BS) {   // uniform
+      const int pos = lo + (q0 + t) / lanes;
+      const bool live = pos < sp.len;
+      v4u p[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        p[r] = v4u{0, 0, 0, 0};
+        if (live && at.at[r] < D)
+          p[r] = *reinterpret_cast<const v4u*>(
+              rows + row_of<true>(x, sp.c0 + pos - p0) * x.ts[0] + at.at[r]);
+      }
+      turned(p, pos);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (live && at.at[r] < D)
+          *reinterpret_cast<v4u*>(tail + (pos & (P - 1)) * D + at.at[r]) = p[r];
+    }
+  }
+}
+
+constexpr int kQueryIt = 2;   // groups of query heads a wave (turn_heads)
+
+template <bool BF, int LAYOUT, int BS, int NU>
+__global__ __launch_bounds__(BS) void cache_append_kernel(Cache c, Sequences s, CacheRows x, HeadArgs a,
+                                                          const uint16_t* k_w, uint32_t page_blocks,
+                                                          int groups) {
+  __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 32];   // a page of values
+  __shared__ float s_turn[LAYOUT == kTurnOdd ? BS / 64 * kTurnRow : 1];
+  __shared__ uint32_t red[BS / 64];
+  const int b = blockIdx.z, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* row = s_turn + (LAYOUT == kTurnOdd ? wave * kTurnRow : 0);
+  if (blockIdx.x < page_blocks) {
+    // heads first: neighbours in a launch read neighbours in memory
+    const uint32_t hk = blockIdx.x % (2 * c.H);
+    const int task = blockIdx.x / (2 * c.H), h = hk >> 1;
+    if (hk & 1) write_page<BF, true, BS, NU, true>(c, s, x, b, h, task, lds, red);
+    else append_keys<BF, LAYOUT, BS, NU>(c, s, x, a, k_w, b, h, task, row, red);
+    return;
+  }
+  const int64_t task = (int64_t)(blockIdx.x - page_blocks) * (BS / 64) + wave;
+  int64_t c0 = s.cu ? s.cu[b] : b, c1 = s.cu ? s.cu[b + 1] : b + 1;
+  c0 = min(max(c0, (int64_t)0), x.rows);
+  c1 = min(max(c1, c0), x.rows);
+  if (x.counts) c1 = min(c1, c0 + max(x.counts[b], 0));
+  const int64_t i = task / groups;
+  if (i >= c1 - c0) return;
+  const int pos = (int)(max(s.lengths[b], 0) - (c1 - c0) + i);
+  turn_heads<BF, LAYOUT, kQueryIt, false>(a, c0 + i, pos, (int)(task % groups), lanes_of(a.D), row,
+                                          threadIdx.x & 63);
+}
+
+namespace {
+template <bool BF, int LAYOUT>
+void launch_append(const Cache& c, const Sequences& s, const CacheRows& x, const HeadArgs& a,
+                   const uint16_t* k_w, int max_new, int max_q, hipStream_t stream) {
+  const uint32_t tasks = (max_new + (1 << c.ps) - 2) / (1 << c.ps) + 1;
+  const uint32_t page_blocks = tasks * 2 * c.H;
+  const int lanes = lanes_of(c.D), per = 64 / lanes * kQueryIt;
+  const int groups = (a.side[0].n + per - 1) / per;
+#define I8L_A(BS, NU, _)                                                                         \
+  hipLaunchKernelGGL((cache_append_kernel<BF, LAYOUT, BS, NU>),                                  \
+                     dim3(page_blocks + (uint32_t)(((int64_t)max_q * groups + BS / 64 - 1) /   \
+                                                   (BS / 64)), 1, s.B),                          \
+                     dim3(BS), 0, stream, c, s, x, a, k_w, page_blocks, groups)
+  I8L_CACHE_SIZES((lanes * 16 << c.ps) / 32, I8L_A, 0);
+#undef I8L_A
+}
+}  // namespace
+
+hipError_t launch_cache_append(const Cache& c, const Sequences& s, const AppendRows& r,
+                               const HeadArgs& a, int max_new, int max_q, hipStream_t stream) {
+  const CacheRows x{{r.k, r.v}, {r.k_ts, r.v_ts}, {r.k_hs, r.v_hs}, r.rows, r.index, r.counts, r.src};
+  const TurnLayout layout = turn_layout(a.turn);
+#define I8L_L(BF)                                                                            \
+  do {                                                                                       \
+    if (layout == kTurnHalves) launch_append<BF, kTurnHalves>(c, s, x, a, r.k_w, max_new, max_q, stream); \
+    else if (layout == kTurnPairs) launch_append<BF, kTurnPairs>(c, s, x, a, r.k_w, max_new, max_q, stream); \
+    else launch_append<BF, kTurnOdd>(c, s, x, a, r.k_w, max_new, max_q, stream);                    \
+  } while (0)
+  if (c.bf16) I8L_L(true);
+  else I8L_L(false);
+#undef I8L_L
+  return hipGetLastError();
+}
+
+}  // namespace i8l

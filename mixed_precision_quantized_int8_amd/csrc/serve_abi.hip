@@ -352,3 +352,295 @@ I8L_API i8l_status int8_cache_attention(const i8l_kv_cache* cache, const i8l_seq
                   static_cast<float*>(workspace), 1, 0};
   return hip_status(fn, i8l::launch_attention(a, static_cast<hipStream_t>(stream)));
 }
+
+// ---- Positions, and drafted tokens over the cache -----------------------------------
+
+namespace {
+
+i8l_status check_head_dim(const char* fn, int D) {
+  if (D < 16 || D > 256 || D % 16)
+    return fail(I8L_ERR_INVALID_ARG, fn, "head_dim=%d must be a multiple of 16 in 16 .. 256", D);
+  return I8L_OK;
+}
+
+i8l_status check_eps(const char* fn, float eps) {
+  if (!(eps >= 0.0f) || isinf(eps))
+    return fail(I8L_ERR_INVALID_ARG, fn, "eps must be finite and >= 0");
+  return I8L_OK;
+}
+
+i8l_status check_rotary(const char* fn, const i8l_rotary* r, int D, i8l::Turn* out) {
+  *out = i8l::Turn{nullptr, 0, false, 1.0f};
+  if (!r) return I8L_OK;
+  if (r->pairs < 0 || 2 * (int64_t)r->pairs > D)
+    return fail(I8L_ERR_INVALID_ARG, fn, "pairs=%d must be in 0 .. head_dim / 2 = %d", r->pairs, D / 2);
+  if (r->interleaved != 0 && r->interleaved != 1)
+    return fail(I8L_ERR_INVALID_ARG, fn, "interleaved=%d must be 0 or 1", r->interleaved);
+  if (!isfinite(r->factor)) return fail(I8L_ERR_INVALID_ARG, fn, "factor must be finite");
+  if (r->pairs) CHECK(check_ptr(fn, "freqs", r->freqs, 4));
+  *out = i8l::Turn{r->freqs, r->pairs, r->interleaved != 0, r->factor};
+  return I8L_OK;
+}
+
+// Waves of a launch over rows of `heads` heads, `per` heads a wave: their threads are
+// counted in 32 bits.
+i8l_status check_launch(const char* fn, int64_t rows, int64_t heads, int D) {
+  const int64_t per = 64 / i8l::lanes_of(D);
+  if (rows * ((heads + per - 1) / per) >= 1 << 24)
+    return fail(I8L_ERR_INVALID_ARG, fn, "%lld rows of %lld heads are too many for one call",
+                (long long)rows, (long long)heads);
+  return I8L_OK;
+}
+
+using Side = i8l::HeadArgs::Side;
+
+i8l_status check_heads(const char* fn, const i8l_heads* h, Side* out) {
+  CHECK(check_count(fn, "heads", h->heads, 1, 65536));
+  CHECK(check_rows(fn, "x", h->x, h->x_token_stride, h->x_head_stride));
+  CHECK(check_rows(fn, "y", h->y, h->y_token_stride, h->y_head_stride));
+  if (h->weight) CHECK(check_ptr(fn, "weight", h->weight, 16));
+  *out = Side{h->x, h->x_token_stride, h->x_head_stride, nullptr, 0, 0, h->y, h->y_token_stride,
+              h->y_head_stride, h->weight, nullptr, h->heads};
+  return I8L_OK;
+}
+
+i8l_status check_heads_grad(const char* fn, const i8l_heads_grad* h, int64_t rows, Side* out) {
+  CHECK(check_count(fn, "heads", h->heads, 1, 65536));
+  if (rows) {
+    CHECK(check_rows(fn, "dy", h->dy, h->dy_token_stride, h->dy_head_stride));
+    CHECK(check_rows(fn, "dx", h->dx, h->dx_token_stride, h->dx_head_stride));
+    if (h->weight) CHECK(check_rows(fn, "x", h->x, h->x_token_stride, h->x_head_stride));
+  }
+  if (h->weight) {
+    CHECK(check_ptr(fn, "weight", h->weight, 16));
+    CHECK(check_ptr(fn, "dweight", h->dweight, 2));
+  }
+  *out = Side{h->x, h->x_token_stride, h->x_head_stride, h->dy, h->dy_token_stride,
+              h->dy_head_stride, h->dx, h->dx_token_stride, h->dx_head_stride, h->weight,
+              h->dweight, h->heads};
+  return I8L_OK;
+}
+
+}  // namespace
+
+I8L_API i8l_status int8_rotate_heads(const i8l_heads* q, const i8l_heads* k, int32_t head_dim,
+                                     int64_t rows, const int32_t* positions,
+                                     const i8l_rotary* rotary, float eps, int dtype,
+                                     void* stream) {
+  const char* fn = "int8_rotate_heads";
+  if (!q) return fail(I8L_ERR_INVALID_ARG, fn, "q is NULL");
+  CHECK(check_dtype(fn, dtype));
+  CHECK(check_head_dim(fn, head_dim));
+  CHECK(check_eps(fn, eps));
+  CHECK(check_count(fn, "rows", rows, 0, INT32_MAX));
+  i8l::HeadArgs a{};
+  CHECK(check_rotary(fn, rotary, head_dim, &a.turn));
+  if (rows == 0) return ok();
+  CHECK(check_heads(fn, q, &a.side[0]));
+  if (k) CHECK(check_heads(fn, k, &a.side[1]));
+  CHECK(check_launch(fn, rows, (int64_t)a.side[0].n + a.side[1].n, head_dim));
+  CHECK_PTR(positions, 4);
+  a.positions = positions;
+  a.rows = (int)rows;
+  a.D = head_dim;
+  a.eps = eps;
+  a.bf16 = dtype == I8L_BF16;
+  (void)hipGetLastError();
+  return hip_status(fn, i8l::launch_rotate_heads(a, static_cast<hipStream_t>(stream)));
+}
+
+I8L_API size_t i8l_rotate_heads_workspace_bytes(int64_t rows, int64_t q_heads, int32_t head_dim) {
+  const char* fn = "i8l_rotate_heads_workspace_bytes";
+  if (check_head_dim(fn, head_dim) != I8L_OK || check_count(fn, "rows", rows, 0, INT32_MAX) != I8L_OK ||
+      check_count(fn, "q_heads", q_heads, 1, 65536) != I8L_OK)
+    return 0;
+  return sizeof(float) * i8l::head_partials((int)rows, (int)q_heads, head_dim);
+}
+
+I8L_API i8l_status int8_rotate_heads_backward(const i8l_heads_grad* q, const i8l_heads_grad* k,
+                                              int32_t head_dim, int64_t rows,
+                                              const int32_t* positions, const i8l_rotary* rotary,
+                                              float eps, int dtype, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+  const char* fn = "int8_rotate_heads_backward";
+  if (!q) return fail(I8L_ERR_INVALID_ARG, fn, "q is NULL");
+  CHECK(check_dtype(fn, dtype));
+  CHECK(check_head_dim(fn, head_dim));
+  CHECK(check_eps(fn, eps));
+  CHECK(check_count(fn, "rows", rows, 0, INT32_MAX));
+  i8l::HeadArgs a{};
+  CHECK(check_rotary(fn, rotary, head_dim, &a.turn));
+  CHECK(check_heads_grad(fn, q, rows, &a.side[0]));
+  if (k) CHECK(check_heads_grad(fn, k, rows, &a.side[1]));
+  CHECK(check_launch(fn, rows, (int64_t)a.side[0].n + a.side[1].n, head_dim));
+  const bool weights = a.side[0].w || a.side[1].w;
+  if (rows == 0 && !weights) return ok();
+  if (rows) CHECK_PTR(positions, 4);
+  if (weights) {
+    const size_t need = sizeof(float) * i8l::head_partials((int)rows, a.side[0].n, head_dim);
+    CHECK_PTR(workspace, 16);
+    if (workspace_bytes < need)
+      return fail(I8L_ERR_WORKSPACE, fn, "workspace has %zu bytes, %zu required", workspace_bytes,
+                  need);
+    a.part = static_cast<float*>(workspace);
+  }
+  a.positions = positions;
+  a.rows = (int)rows;
+  a.D = head_dim;
+  a.eps = eps;
+  a.bf16 = dtype == I8L_BF16;
+  (void)hipGetLastError();
+  return hip_status(fn, i8l::launch_rotate_heads_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+I8L_API i8l_status int8_cache_append(const i8l_kv_cache* cache, const i8l_sequences* seqs,
+                                     const int32_t* counts, const int32_t* index,
+                                     const uint16_t* k, int64_t k_token_stride,
+                                     int64_t k_head_stride, const uint16_t* v,
+                                     int64_t v_token_stride, int64_t v_head_stride,
+                                     int64_t kv_rows, int64_t rows, int64_t max_new,
+                                     const i8l_heads* q, const uint16_t* k_weight,
+                                     const i8l_rotary* rotary, float eps, void* stream) {
+  const char* fn = "int8_cache_append";
+  i8l::Cache c;
+  i8l::Sequences s;
+  i8l::HeadArgs a{};
+  CHECK(check_cache(fn, cache, &c));
+  CHECK(check_seqs(fn, seqs, c.ps, false, &s));
+  CHECK(check_rotary(fn, rotary, c.D, &a.turn));
+  CHECK(check_eps(fn, eps));
+  CHECK(check_count(fn, "rows", rows, 0, kMaxRows));
+  CHECK(check_count(fn, "kv_rows", kv_rows, 0, kMaxRows));
+  CHECK(check_count(fn, "max_new", max_new, 0, kMaxTokens));
+  if (index && q) return fail(I8L_ERR_INVALID_ARG, fn, "q must be NULL with an index");
+  if (rows == 0 || max_new == 0 || s.B == 0) return ok();
+  if (s.max_pages == 0)   // (queries would still be turned)
+    return fail(I8L_ERR_INVALID_ARG, fn, "max_pages=0 with %d sequences", s.B);
+  if (kv_rows < (index ? 1 : rows))
+    return fail(I8L_ERR_INVALID_ARG, fn, "kv_rows=%lld with rows=%lld", (long long)kv_rows,
+                (long long)rows);
+  CHECK(check_rows(fn, "k", k, k_token_stride, k_head_stride));
+  CHECK(check_rows(fn, "v", v, v_token_stride, v_head_stride));
+  if (counts) CHECK_PTR(counts, 4);
+  if (index) CHECK_PTR(index, 4);
+  if (k_weight) CHECK_PTR(k_weight, 16);
+  if (q) CHECK(check_heads(fn, q, &a.side[0]));
+  const int64_t most = std::min(max_new, rows);
+  // no sequence gets more tokens than its pages hold
+  max_new = std::min(most, (int64_t)s.max_pages << c.ps);
+  CHECK(check_pages(fn, c, 2 * max_new));   // (half of what a launch counts, the queries the rest)
+  if (q) CHECK(check_launch(fn, 2 * most, q->heads, c.D));
+  a.D = c.D;
+  a.eps = eps;
+  a.bf16 = c.bf16;
+  const i8l::AppendRows x{k, v, k_weight, k_token_stride, k_head_stride, v_token_stride,
+                          v_head_stride, kv_rows, rows, index, counts};
+  (void)hipGetLastError();
+  return hip_status(fn, i8l::launch_cache_append(c, s, x, a, (int)max_new, (int)most,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+i8l_status check_tree(const char* fn, const i8l::TreeRows& t, int64_t n, int64_t max_q) {
+  CHECK(check_count(fn, "n", n, 0, 65535));
+  CHECK(check_count(fn, "rows", t.rows, 0, INT32_MAX));
+  CHECK(check_count(fn, "max_q", max_q, 1, i8l::kMaxDrafts));
+  return I8L_OK;
+}
+
+i8l_status check_tree_arrays(const char* fn, const i8l::TreeRows& t) {
+  if (t.rows) CHECK(check_ptr(fn, "parents", t.parents, 4));
+  CHECK(check_ptr(fn, "lengths", t.lengths, 4));
+  if (t.cu) CHECK(check_ptr(fn, "cu", t.cu, 4));
+  return I8L_OK;
+}
+
+static_assert(I8L_MAX_DRAFTS == i8l::kMaxDrafts, "the header's limit");
+
+}  // namespace
+
+I8L_API i8l_status int8_tree_plan(const int32_t* parents, const int32_t* lengths, const int32_t* cu,
+                                  int64_t n, int64_t rows, int64_t max_q, int32_t* positions,
+                                  uint64_t* masks, int32_t words, void* stream) {
+  const char* fn = "int8_tree_plan";
+  const i8l::TreeRows t{parents, lengths, cu, rows, (int)n, (int)max_q};
+  CHECK(check_tree(fn, t, n, max_q));
+  CHECK(check_count(fn, "words", words, (max_q + 63) / 64, i8l::kMaxDrafts / 64));
+  if (n == 0 || rows == 0) return ok();
+  CHECK(check_tree_arrays(fn, t));
+  CHECK_PTR(positions, 4);
+  CHECK_PTR(masks, 8);
+  (void)hipGetLastError();
+  return hip_status(fn, i8l::launch_tree_plan(t, positions, masks, words,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+I8L_API i8l_status int8_tree_attention(
+    const i8l_kv_cache* cache, const i8l_sequences* seqs, const uint16_t* q, int64_t q_token_stride,
+    int64_t q_head_stride, int64_t q_heads, const uint16_t* k, int64_t k_token_stride,
+    int64_t k_head_stride, const uint16_t* v, int64_t v_token_stride, int64_t v_head_stride,
+    int64_t rows, int64_t max_q, int64_t max_len, const uint64_t* masks, int32_t words,
+    const int32_t* positions, float scale, int64_t window, const float* alibi, uint16_t* out,
+    void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "int8_tree_attention";
+  i8l::Cache c;
+  i8l::Sequences s;
+  CHECK(check_cache(fn, cache, &c));
+  CHECK(check_seqs(fn, seqs, c.ps, false, &s));
+  CHECK(check_attention(fn, c, q_heads, max_q, max_len, window));
+  CHECK(check_count(fn, "rows", rows, 0, kMaxRows));
+  CHECK(check_count(fn, "words", words, 1, i8l::kMaxDrafts / 64));
+  CHECK(check_count(fn, "max_q", max_q, 1, 64 * words));
+  if (!isfinite(scale)) return fail(I8L_ERR_INVALID_ARG, fn, "scale must be finite");
+  if (rows == 0 || s.B == 0) return ok();
+  if (s.max_pages == 0)   // the kernels read the arrays of every sequence
+    return fail(I8L_ERR_INVALID_ARG, fn, "max_pages=0 with %d sequences", s.B);
+  CHECK(check_rows(fn, "q", q, q_token_stride, q_head_stride));
+  CHECK(check_rows(fn, "k", k, k_token_stride, k_head_stride));
+  CHECK(check_rows(fn, "v", v, v_token_stride, v_head_stride));
+  CHECK_PTR(masks, 8);
+  CHECK_PTR(out, 16);
+  if (alibi) CHECK_PTR(alibi, 4);
+  if (positions || alibi || window) CHECK_PTR(positions, 4);
+  window = std::min(window, kMaxTokens);
+  const int G = (int)(q_heads / c.H);
+  const size_t need = sizeof(float) * i8l::attention_partials(s.B, c.H, G, c.D, (int)max_q,
+                                                              (int)max_len, (int)window);
+  if (need) {
+    CHECK_PTR(workspace, 16);
+    if (workspace_bytes < need)
+      return fail(I8L_ERR_WORKSPACE, fn, "workspace has %zu bytes, %zu required", workspace_bytes,
+                  need);
+  }
+  (void)hipGetLastError();
+  const i8l::TreeArgs a{{c, s, q, q_token_stride, q_head_stride, out, rows, G, (int)max_q,
+                         (int)max_len, (int)window, scale, alibi, static_cast<float*>(workspace), 1, 0},
+                        masks, words, positions, k, v, k_token_stride, k_head_stride,
+                        v_token_stride, v_head_stride};
+  return hip_status(fn, i8l::launch_tree_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+I8L_API i8l_status int8_tree_accept(const int32_t* parents, const int64_t* tokens,
+                                    const int64_t* choices, const int64_t* first,
+                                    const int32_t* lengths, const int32_t* cu, int64_t n,
+                                    int64_t rows, int64_t max_q, int32_t* path, int32_t* counts,
+                                    int32_t* new_lengths, int64_t* next, void* stream) {
+  const char* fn = "int8_tree_accept";
+  const i8l::TreeRows t{parents, lengths, cu, rows, (int)n, (int)max_q};
+  CHECK(check_tree(fn, t, n, max_q));
+  if (n == 0) return ok();
+  CHECK(check_tree_arrays(fn, t));
+  if (rows) {
+    CHECK_PTR(tokens, 8);
+    CHECK_PTR(choices, 8);
+    CHECK_PTR(path, 4);
+  }
+  if (first) CHECK_PTR(first, 8);
+  CHECK_PTR(counts, 4);
+  CHECK_PTR(new_lengths, 4);
+  CHECK_PTR(next, 8);
+  (void)hipGetLastError();
+  return hip_status(fn, i8l::launch_tree_accept(t, tokens, choices, first, path, counts, new_lengths,
+                                                next, static_cast<hipStream_t>(stream)));
+}

@@ -5,6 +5,9 @@ feeds them, the key/value cache and the attention over it, as they run together.
     cache = new_cache(n_pages, n_slots, kv_heads, head_dim)
     y, r = layer(x, None, cache, page_table, lengths, cu, max_q=..., max_len=...)  # prompts
     y, r = layer(x, None, cache, page_table, lengths)                              # one token each
+    # trees of drafted tokens (tree_plan), then the accepted ones (tree_accept) into the cache
+    y, r, kv = layer.draft(x, None, cache, page_table, lengths, positions, masks, cu)
+    layer.accept(kv, cache, page_table, new_lengths, path, counts, cu)
 
 Pre-norm: r = x + residual, a = out(attention(qkv(norm1(r)))), r' = r + a,
 y = down(gelu(up(norm2(r')))); the caller passes (y, r') on to the next layer,
@@ -17,7 +20,8 @@ makes its steps 0.47, an error of 14 % of each unit value where rows without
 outlier columns have about 1 %.  That path is for models whose normed rows have
 none; it takes 0.58 ms instead of 0.80 for a prompt of 2048 rows, 0.16 instead of
 0.27 for 16 single tokens (hidden 4096, 32 heads of 128 on 8, 16384 features in
-between).  Positions enter as linear biases (``alibi``) or not at all.  What has no
+between).  Positions enter as linear biases (``alibi``), by rotation of queries and keys
+(``rotary``; with norms of their heads, if given), or not at all.  What has no
 kernel in the library, the norm to 16 bits and the activation function, is torch's.
 """
 from __future__ import annotations
@@ -26,6 +30,7 @@ import torch
 
 from . import quantize_weight as _quantize_weight
 from .module import Int8Linear
+from .positions import cache_append, rotate_heads, tree_attention
 from .serving import _inference, cache_attention, cache_write, linear_codes, rmsnorm_quant
 
 
@@ -55,11 +60,12 @@ class Int8DecoderLayer(torch.nn.Module):
     rows of outlier columns (False: those rows are rebuilt from the codes, which saves two
     bytes a weight; a code's rounding, about 1 % of a feature's weights, is then
     multiplied by the outlier).  ``codes``: qkv and up on the norm's row codes, with no
-    outlier columns."""
+    outlier columns.  ``rotary``: a ``Rotary`` for queries and keys; ``q_norm`` and ``k_norm``
+    [head_dim]: the weights of their heads' norms (eps ``head_eps``)."""
 
     def __init__(self, norm1, qkv, out, norm2, up, down, heads, kv_heads=None, alibi=None,
                  eps=1e-5, threshold=6.0, device="cuda", codes=False,
-                 has_fp16_weights=True):
+                 has_fp16_weights=True, rotary=None, q_norm=None, k_norm=None, head_eps=1e-6):
         super().__init__()
         kv_heads = heads if kv_heads is None else kv_heads
         hidden = qkv.in_features
@@ -84,6 +90,10 @@ class Int8DecoderLayer(torch.nn.Module):
         self.out, self.down = product(out), product(down)
         self.register_buffer("alibi", None if alibi is None else
                              torch.as_tensor(alibi, dtype=torch.float32).to(device))
+        self.rotary, self.head_eps = rotary, head_eps
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            self.register_buffer(name, None if w is None else w.detach().to(device, torch.float16))
+        self._turned = any(x is not None for x in (rotary, q_norm, k_norm))
 
     def _norm_product(self, lin, x, residual, weight):
         """(lin(norm of r), r), r = x + residual."""
@@ -102,12 +112,49 @@ class Int8DecoderLayer(torch.nn.Module):
         included), cu, slots, max_q and max_len as for ``cache_attention``."""
         _inference(x, residual)
         with torch.no_grad():
-            rows, D, H = x.shape[0], self.head_dim, self.heads
-            qkv, r = self._norm_product(self.qkv, x, residual, self.norm1)
-            qkv = qkv.view(rows, H + 2 * self.kv_heads, D)
-            q, k, v = qkv[:, :H], qkv[:, H:H + self.kv_heads], qkv[:, H + self.kv_heads:]
-            cache_write(cache, k, v, page_table, lengths, cu=cu, slots=slots, max_new=max_q)
+            q, k, v, r = self._heads(x, residual)
+            if self._turned:
+                q = cache_append(cache, k, v, page_table, lengths, q=q, rotary=self.rotary,
+                                 q_weight=self.q_norm, k_weight=self.k_norm, eps=self.head_eps, cu=cu,
+                                 slots=slots, max_new=max_q, q_out=q)
+            else:
+                cache_write(cache, k, v, page_table, lengths, cu=cu, slots=slots, max_new=max_q)
             a = cache_attention(q, cache, page_table, lengths, cu=cu, slots=slots, max_q=max_q,
                                 max_len=max_len, window=window, alibi=self.alibi)
-            up, r = self._norm_product(self.up, self.out(a.view(rows, H * D)), r, self.norm2)
-            return self.down(torch.nn.functional.gelu(up)), r
+            return self._rest(a, r)
+
+    def draft(self, x, residual, cache, page_table, lengths, positions, masks, cu=None, slots=None,
+              max_q=None, max_len=None, window=0):
+        """(y, r', kv) of rows x (+ residual) that are drafted tokens, trees of them behind
+        their sequences: lengths counts the cached tokens alone, positions and masks are
+        ``tree_plan``'s, the rest as for ``tree_attention``.  The cache is left as it is;
+        kv, the rows' keys and values, is for ``accept``."""
+        _inference(x, residual)
+        with torch.no_grad():
+            q, k, v, r = self._heads(x, residual)
+            if self._turned:
+                q, k = rotate_heads(q, positions, self.rotary, k=k, q_weight=self.q_norm,
+                                    k_weight=self.k_norm, eps=self.head_eps, q_out=q, k_out=k)
+            a = tree_attention(q, k, v, cache, page_table, lengths, masks, positions=positions, cu=cu,
+                               slots=slots, max_q=max_q, max_len=max_len, window=window,
+                               alibi=self.alibi)
+            return (*self._rest(a, r), (k, v))
+
+    def accept(self, kv, cache, page_table, lengths, path, counts, cu=None, slots=None, max_new=None):
+        """Appends the accepted drafts among kv to the cache: path, counts and lengths (the
+        new ones) as ``tree_accept`` gives them."""
+        cache_append(cache, *kv, page_table, lengths, cu=cu, slots=slots, max_new=max_new,
+                     counts=counts, index=path)
+
+    def _heads(self, x, residual):
+        """(q, k, v, r): heads of the rows, before norm and rotation."""
+        D, H = self.head_dim, self.heads
+        qkv, r = self._norm_product(self.qkv, x, residual, self.norm1)
+        qkv = qkv.view(x.shape[0], H + 2 * self.kv_heads, D)
+        return qkv[:, :H], qkv[:, H:H + self.kv_heads], qkv[:, H + self.kv_heads:], r
+
+    def _rest(self, a, r):
+        """(y, r') from the attention's output on."""
+        a = self.out(a.view(a.shape[0], self.heads * self.head_dim))
+        up, r = self._norm_product(self.up, a, r, self.norm2)
+        return self.down(torch.nn.functional.gelu(up)), r

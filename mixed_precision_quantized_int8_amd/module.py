@@ -12,8 +12,11 @@ passes gradients through unchanged), on the library's fp16 kernels.  Every
 model layer except the output head is replaced (the blog keeps ``lm_head`` in
 full precision).
 
-The module only holds tensors and calls the library: quantization, the layer,
-the bias and the gradients all run in the HIP kernels.
+``RotateHeads`` is the norm and rotary rotation of query and key heads between such
+layers, with its gradients.
+
+The modules only hold tensors and call the library: quantization, the layer,
+the bias, the rotation and the gradients all run in the HIP kernels.
 """
 from __future__ import annotations
 
@@ -24,6 +27,8 @@ from . import backward_input as _backward_input
 from . import backward_weight as _backward_weight
 from . import linear as _linear
 from . import quantize_weight as _quantize_weight
+from . import rotate_heads as _rotate_heads
+from . import rotate_heads_backward as _rotate_heads_backward
 
 
 class _Int8LinearFn(torch.autograd.Function):
@@ -132,6 +137,56 @@ class Int8Linear(torch.nn.Module):
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"bias={self.bias is not None}, has_fp16_weights={self.has_fp16_weights}, "
                 f"threshold={self.threshold}")
+
+
+class _RotateHeadsFn(torch.autograd.Function):
+    """(q', k') of rotate_heads, with its gradients (first order)."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, rotary, q_weight, k_weight, eps):
+        out = _rotate_heads(q, positions, rotary, k=k, q_weight=q_weight, k_weight=k_weight, eps=eps)
+        # without a norm the gradient does not depend on what went in
+        ctx.save_for_backward(positions, q if q_weight is not None else None,
+                              k if k_weight is not None else None, q_weight, k_weight)
+        ctx.rotary, ctx.eps, ctx.two = rotary, eps, k is not None
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        positions, q, k, q_weight, k_weight = ctx.saved_tensors
+        dq, dk, dqw, dkw = _rotate_heads_backward(
+            grads[0].contiguous(), positions, ctx.rotary, q=q,
+            dk=grads[1].contiguous() if ctx.two else None, k=k, q_weight=q_weight, k_weight=k_weight,
+            eps=ctx.eps)
+        return dq, dk, None, None, dqw, dkw, None
+
+
+class RotateHeads(torch.nn.Module):
+    """Norm of each query and key head and rotary rotation, with gradients: (q', k') of
+    q [rows][heads][head_dim], k [rows][kv_heads][head_dim] and positions int32 [rows]
+    (q' alone without k).
+
+    ``rotary``: a ``Rotary``, or None for the norms alone.  With ``norm`` the parameters
+    ``q_weight`` and ``k_weight`` [head_dim] (ones at first) scale the normed heads; they and
+    the tensors share one type, fp16 or bf16.
+    """
+
+    def __init__(self, head_dim: int, rotary=None, norm: bool = True, eps: float = 1e-6,
+                 dtype=torch.float16, device=None):
+        super().__init__()
+        dev = torch.device(device) if device is not None else torch.device("cuda")
+        self.head_dim, self.rotary, self.eps = head_dim, rotary, float(eps)
+        for name in ("q_weight", "k_weight"):
+            w = torch.nn.Parameter(torch.ones((head_dim,), dtype=dtype, device=dev)) if norm else None
+            self.register_parameter(name, w)
+
+    def forward(self, q, positions, k=None):
+        return _RotateHeadsFn.apply(q, k, positions, self.rotary, self.q_weight,
+                                    self.k_weight if k is not None else None, self.eps)
+
+    def extra_repr(self) -> str:
+        return f"head_dim={self.head_dim}, norm={self.q_weight is not None}, eps={self.eps}"
 
 
 def replace_linear(model: torch.nn.Module, skip=("lm_head",), has_fp16_weights: bool = False,
