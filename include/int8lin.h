@@ -484,7 +484,7 @@ typedef struct {
 
 /* Workspace bytes of int8_rotate_heads_backward where q or k has a weight (0: sizes
  * that it refuses); without weights it needs none. */
-size_t i8l_rotate_heads_workspace_bytes(int64_t rows, int64_t q_heads, int32_t head_dim);
+size_t i8l_rotate_heads_workspace_bytes(int64_t rows, int32_t head_dim);
 
 /* rows == 0: dweight = 0.  workspace: 16-byte aligned. */
 i8l_status int8_rotate_heads_backward(const i8l_heads_grad *q, const i8l_heads_grad *k,

@@ -223,7 +223,7 @@ def lib() -> ctypes.CDLL:
     i32 = ctypes.c_int32
     L.int8_rotate_heads.argtypes = [heads, heads, i32, i64, vp, rot, f32, ctypes.c_int, vp]
     L.int8_rotate_heads.restype = ctypes.c_int
-    L.i8l_rotate_heads_workspace_bytes.argtypes = [i64, i64, i32]
+    L.i8l_rotate_heads_workspace_bytes.argtypes = [i64, i32]
     L.i8l_rotate_heads_workspace_bytes.restype = sz
     L.int8_rotate_heads_backward.argtypes = [grads, grads, i32, i64, vp, rot, f32, ctypes.c_int, vp,
                                              sz, vp]

@@ -32,6 +32,7 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   uint16_t* tail = c.kt + ((size_t)(slot_ok ? slot : 0) * c.H + h) * P * D;
   const uint16_t* rows = x.x[0] + h * x.hs[0];
   const Runs at = runs_of<LAYOUT>(a.turn, j);
+  const float inv = 1.0f / (float)D;
   v4u w[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -42,9 +43,16 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   auto turned = [&](v4u (&p)[2], int pos) {
     float y[16];
     unpack<BF>(p, y);
-    if (k_w) normed<BF>(y, w, rms_of<BF>(y, D, lanes, a.eps));
+    if (k_w) {
+      const Rms m = rms_of<BF>(y, inv, lanes, a.eps);
+      float wf[16];
+      unpack<BF>(w, wf);
+      over_rms(y, m);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] *= wf[e];
+    }
     Angles<LAYOUT> angles;
-    angles.of(a.turn, j, pos, false);
+    angles.of(a.turn, j, false, [&](int i) { return angle(pos, a.turn.freqs[i], a.turn.factor); });
     turn<LAYOUT>(y, angles, a.turn, j, row, lane);
     pack<BF>(y, p);
   };
@@ -138,17 +146,17 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   }
 }
 
-constexpr int kQueryIt = 2;   // groups of query heads a wave (turn_heads)
-
 template <bool BF, int LAYOUT, int BS, int NU>
 __global__ __launch_bounds__(BS) void cache_append_kernel(Cache c, Sequences s, CacheRows x, HeadArgs a,
                                                           const uint16_t* k_w, uint32_t page_blocks,
-                                                          int groups) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 32];   // a page of values
+                                                          int n_tok, int groups, int per_wg) {
+  // a page of values, or the angles of a workgroup's queries
+  __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 32];
+  static_assert(sizeof(lds) >= 2048, "kTurnTokens * 64 angles; 128 come with twice the threads");
   __shared__ float s_turn[LAYOUT == kTurnOdd ? BS / 64 * kTurnRow : 1];
   __shared__ uint32_t red[BS / 64];
-  const int b = blockIdx.z, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  float* row = s_turn + (LAYOUT == kTurnOdd ? wave * kTurnRow : 0);
+  const int b = blockIdx.z;
+  float* row = s_turn + (LAYOUT == kTurnOdd ? (threadIdx.x >> 6) * kTurnRow : 0);
   if (blockIdx.x < page_blocks) {
     // heads first: neighbours in a launch read neighbours in memory
     const uint32_t hk = blockIdx.x % (2 * c.H);
@@ -157,32 +165,40 @@ __global__ __launch_bounds__(BS) void cache_append_kernel(Cache c, Sequences s, 
     else append_keys<BF, LAYOUT, BS, NU>(c, s, x, a, k_w, b, h, task, row, red);
     return;
   }
-  const int64_t task = (int64_t)(blockIdx.x - page_blocks) * (BS / 64) + wave;
+  const uint32_t parts = (groups + per_wg - 1) / per_wg, q = blockIdx.x - page_blocks;
   int64_t c0 = s.cu ? s.cu[b] : b, c1 = s.cu ? s.cu[b + 1] : b + 1;
   c0 = min(max(c0, (int64_t)0), x.rows);
   c1 = min(max(c1, c0), x.rows);
   if (x.counts) c1 = min(c1, c0 + max(x.counts[b], 0));
-  const int64_t i = task / groups;
-  if (i >= c1 - c0) return;
-  const int pos = (int)(max(s.lengths[b], 0) - (c1 - c0) + i);
-  turn_heads<BF, LAYOUT, kQueryIt, false>(a, c0 + i, pos, (int)(task % groups), lanes_of(a.D), row,
-                                          threadIdx.x & 63);
+  const int64_t i0 = (int64_t)(q / parts) * n_tok;
+  if (i0 >= c1 - c0) return;
+  const int g0 = q % parts * per_wg, pos0 = (int)(max(s.lengths[b], 0) - (c1 - c0) + i0);
+  turn_heads<BF, LAYOUT, BS / 64, false>(
+      a, c0 + i0, (int)min((int64_t)n_tok, c1 - c0 - i0), [&](int i) { return pos0 + i; }, g0,
+      min(per_wg, groups - g0), lanes_of(a.D), reinterpret_cast<float2*>(lds), row);
 }
 
 namespace {
+template <bool BF, int LAYOUT, int BS, int NU>
+void launch_sized(const Cache& c, const Sequences& s, const CacheRows& x, const HeadArgs& a,
+                  const uint16_t* k_w, uint32_t page_blocks, int max_q, hipStream_t stream) {
+  // the queries' workgroups, as launch_rows has them
+  const int per = 64 / lanes_of(c.D), groups = (a.side[0].n + per - 1) / per;
+  const int n_tok = max_q >= 2048 ? kTurnTokens : 1;
+  const int per_wg = n_tok == 1 && groups > BS / 64 && (int64_t)max_q * s.B * groups < 8192 ? BS / 64 : groups;
+  const uint32_t q_blocks =
+      groups ? (uint32_t)((max_q + n_tok - 1) / n_tok * ((groups + per_wg - 1) / per_wg)) : 0;
+  hipLaunchKernelGGL((cache_append_kernel<BF, LAYOUT, BS, NU>), dim3(page_blocks + q_blocks, 1, s.B),
+                     dim3(BS), 0, stream, c, s, x, a, k_w, page_blocks, n_tok, groups, per_wg);
+}
+
 template <bool BF, int LAYOUT>
 void launch_append(const Cache& c, const Sequences& s, const CacheRows& x, const HeadArgs& a,
                    const uint16_t* k_w, int max_new, int max_q, hipStream_t stream) {
   const uint32_t tasks = (max_new + (1 << c.ps) - 2) / (1 << c.ps) + 1;
   const uint32_t page_blocks = tasks * 2 * c.H;
-  const int lanes = lanes_of(c.D), per = 64 / lanes * kQueryIt;
-  const int groups = (a.side[0].n + per - 1) / per;
-#define I8L_A(BS, NU, _)                                                                         \
-  hipLaunchKernelGGL((cache_append_kernel<BF, LAYOUT, BS, NU>),                                  \
-                     dim3(page_blocks + (uint32_t)(((int64_t)max_q * groups + BS / 64 - 1) /   \
-                                                   (BS / 64)), 1, s.B),                          \
-                     dim3(BS), 0, stream, c, s, x, a, k_w, page_blocks, groups)
-  I8L_CACHE_SIZES((lanes * 16 << c.ps) / 32, I8L_A, 0);
+#define I8L_A(BS, NU, _) launch_sized<BF, LAYOUT, BS, NU>(c, s, x, a, k_w, page_blocks, max_q, stream)
+  I8L_CACHE_SIZES((lanes_of(c.D) * 16 << c.ps) / 32, I8L_A, 0);
 #undef I8L_A
 }
 }  // namespace

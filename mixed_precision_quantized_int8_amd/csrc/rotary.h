@@ -1,6 +1,6 @@
 // Norm and rotary rotation of one head in registers (internal header): shared by
 // the row kernels (rotate.hip) and the cache's (append.hip), which therefore give the
-// same bits.
+// same bits (sums of products are explicit fused operations, not the compiler's choice).
 //
 //   n_d = x_d / sqrt(mean x^2 + eps) * w_d     (without a weight: x_d),
 //   pair (a, b) of frequency i, t = position * freqs[i], f a common factor:
@@ -42,31 +42,24 @@ __device__ __forceinline__ Runs runs_of(const Turn& r, int j) {
 
 // cos and sin (times the factor) of one pair's angle.  position * freq is formed in 64
 // bits, since at position 10^6 a 32-bit product is off by 0.06 radians, and reduced to
-// a quarter turn there; then Taylor's series over |x| <= pi / 4 (the first terms left
-// out, x^11 / 11! and x^10 / 10!, are below 2^-25).
-__device__ __forceinline__ void angle(int pos, float freq, float f, float* c, float* s) {
+// half a turn there; the hardware's sine and cosine of turns are then within 1.3e-7
+// (measured over that range), and a third of the time of a series.
+__device__ __forceinline__ float2 angle(int pos, float freq, float f) {
+#pragma clang fp contract(off)   // (the same bits wherever it is inlined)
   double t = (double)pos * (double)freq * 0.15915494309189533577;   // turns
   t -= __builtin_rint(t);
   const float u = (float)t;                          // -1/2 .. 1/2
-  const float q = __builtin_rintf(4.0f * u);
-  const float x = (float)(t - 0.25 * (double)q) * 6.28318530717958647693f;
-  const float z = x * x;
-  const float sx = x + x * z * (-1.0f / 6 + z * (1.0f / 120 + z * (-1.0f / 5040 + z * (1.0f / 362880))));
-  const float cx = 1.0f + z * (-0.5f + z * (1.0f / 24 + z * (-1.0f / 720 + z * (1.0f / 40320))));
-  const int n = (int)q;                              // quarter turns, -2 .. 2
-  const bool odd = n & 1;
-  const float cc = odd ? sx : cx, ss = odd ? cx : sx;
-  *c = f * ((n + 1) & 2 ? -cc : cc);
-  *s = f * (n & 2 ? -ss : ss);
+  return make_float2(f * __builtin_amdgcn_cosf(u), f * __builtin_amdgcn_sinf(u));
 }
 
-// The 8 (kTurnOdd: 16) angles of a thread; an element past the pairs has angle 0 and
-// factor 1.  `back`: the other way.
+// The 8 (kTurnOdd: 16) angles of a thread, each from `get(i)`, pair i's cos and sin; an
+// element past the pairs has angle 0 and factor 1.  `back`: the other way.
 template <int LAYOUT>
 struct Angles {
   static constexpr int N = LAYOUT == kTurnOdd ? 16 : 8;
   float c[N], s[N];
-  __device__ __forceinline__ void of(const Turn& r, int j, int pos, bool back) {
+  template <class Get>
+  __device__ __forceinline__ void of(const Turn& r, int j, bool back, Get get) {
     const int h = r.pairs;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -79,10 +72,10 @@ struct Angles {
         second = d >= h;
         i = second ? d - h : d;
       }
-      c[e] = 1.0f;
-      s[e] = 0.0f;
-      if (on) angle(pos, r.freqs[i], r.factor, &c[e], &s[e]);
-      if (back) s[e] = -s[e];
+      float2 a = make_float2(1.0f, 0.0f);
+      if (on) a = get(i);
+      c[e] = a.x;
+      s[e] = back ? -a.y : a.y;
       if (LAYOUT == kTurnOdd && !second) s[e] = -s[e];   // y_a = a c + b (-s), y_b = b c + a s
     }
   }
@@ -99,16 +92,16 @@ __device__ __forceinline__ void turn(float (&x)[16], const Angles<LAYOUT>& a, co
     for (int e = 0; e < 8; ++e) {
       const float p = x[e], q = x[8 + e];
       if (8 * j < r.pairs) {
-        x[e] = p * a.c[e] - q * a.s[e];
-        x[8 + e] = p * a.s[e] + q * a.c[e];
+        x[e] = __builtin_fmaf(p, a.c[e], -(q * a.s[e]));
+        x[8 + e] = __builtin_fmaf(p, a.s[e], q * a.c[e]);
       }
     }
   } else if constexpr (LAYOUT == kTurnPairs) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float p = x[2 * e], q = x[2 * e + 1];
-      x[2 * e] = p * a.c[e] - q * a.s[e];
-      x[2 * e + 1] = p * a.s[e] + q * a.c[e];
+      x[2 * e] = __builtin_fmaf(p, a.c[e], -(q * a.s[e]));
+      x[2 * e + 1] = __builtin_fmaf(p, a.s[e], q * a.c[e]);
     }
   } else {
     // (a wave's LDS accesses are done in order; no other wave uses this part)
@@ -123,7 +116,7 @@ __device__ __forceinline__ void turn(float (&x)[16], const Angles<LAYOUT>& a, co
     for (int e = 0; e < 16; ++e) {
       const int d = 16 * j + e;
       const int other = d < r.pairs ? d + r.pairs : d < 2 * r.pairs ? d - r.pairs : d;
-      x[e] = x[e] * a.c[e] + head[other + (other >> 4)] * a.s[e];
+      x[e] = __builtin_fmaf(x[e], a.c[e], head[other + (other >> 4)] * a.s[e]);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -143,19 +136,28 @@ __device__ __forceinline__ void pack(const float (&x)[16], v4u (&p)[2]) {
   for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = pack2<BF>(x[2 * i], x[2 * i + 1]);
 }
 
-__device__ __forceinline__ float head_sum(float v, int lanes) {   // over a head's lanes
-  for (int off = 1; off < lanes; off <<= 1) v += __shfl_xor(v, off, 64);
+// The sum over a head's lanes (up to 16 neighbours), in all of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf,
+                                                               0xf, true));
+}
+__device__ __forceinline__ float head_sum(float v, int lanes) {
+  if (lanes > 1) v += dpp<0xb1>(v);     // neighbours
+  if (lanes > 2) v += dpp<0x4e>(v);     // pairs
+  if (lanes > 4) v += dpp<0x141>(v);    // fours, mirrored within 8: all of a four hold the same
+  if (lanes > 8) v += dpp<0x140>(v);    // eights, mirrored within 16
   return v;
 }
 
 // 1 / rms of a head is pre * r: pre is 1 unless squares of bf16 leave fp32's range
 // (then a power of two that brings them back).  A head of zeros gets 0 for any eps.
-// Every lane of the wave takes part.
+// Every lane of the wave takes part.  inv: 1 / D.
 struct Rms {
   float pre, r;
 };
 template <bool BF>
-__device__ __forceinline__ Rms rms_of(const float (&x)[16], int D, int lanes, float eps) {
+__device__ __forceinline__ Rms rms_of(const float (&x)[16], float inv, int lanes, float eps) {
   float sum = 0.0f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) sum = __builtin_fmaf(x[e], x[e], sum);
@@ -174,64 +176,103 @@ __device__ __forceinline__ Rms rms_of(const float (&x)[16], int D, int lanes, fl
       sum = head_sum(sum, lanes);
     }
   }
-  const float mean = sum / (float)D + eps * pre * pre;
-  return Rms{pre, mean == 0.0f ? 0.0f : 1.0f / __builtin_sqrtf(mean)};
+  const float mean = __builtin_fmaf(sum, inv, eps * pre * pre);
+  return Rms{pre, mean < 0x1p-126f ? 0.0f : __builtin_amdgcn_rsqf(mean)};
 }
-
-template <bool BF>
-__device__ __forceinline__ void normed(float (&x)[16], const v4u (&w)[2], const Rms& m) {
-  float wf[16];
-  unpack<BF>(w, wf);
+// x / rms; a NaN stays one.
+__device__ __forceinline__ void over_rms(float (&x)[16], const Rms& m) {
+  if (__any(m.pre != 1.0f)) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = x[e] * m.pre * m.r * wf[e];
+    for (int e = 0; e < 16; ++e) x[e] *= m.pre;
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] *= m.r;
 }
 
-// The heads of one token: a wave takes 64 / lanes_of(D) of them at a time, IT times
-// (`group` counts these), so that the angles are formed once for all.  `back`: the
-// gradient without a norm, dy turned the other way.
-template <bool BF, int LAYOUT, int IT, bool BACK>
-__device__ __forceinline__ void turn_heads(const HeadArgs& a, int64_t tok, int pos, int group,
-                                           int lanes, float* row, int lane) {
-  const int j = lane & (lanes - 1), per = 64 / lanes;
-  const int head0 = group * per * IT + lane / lanes;
-  const int n0 = a.side[0].n, all = n0 + a.side[1].n, D = a.D;
+// The heads of some tokens, by a workgroup of NW waves: tok0 .. tok0 + n_tok - 1 at
+// positions pos(0) .. pos(n_tok - 1), the groups of 64 / lanes_of(D) heads from g0 on, ng
+// of them.  The angles are formed once, into s_cs (n_tok * pairs), and a wave takes a token's
+// group at a time, with the next one's elements on their way.  BACK: the gradient without
+// a norm, dy turned the other way.
+constexpr int kTurnTokens = 4;   // at most n_tok
+constexpr int kMaxPairs = 128;
+template <bool BF, int LAYOUT, int NW, bool BACK, class Pos>
+__device__ __forceinline__ void turn_heads(const HeadArgs& a, int64_t tok0, int n_tok, Pos pos, int g0,
+                                           int ng, int lanes, float2* s_cs, float* row) {
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int j = lane & (lanes - 1), sub = lane / lanes, per = 64 / lanes;
+  const int n0 = a.side[0].n, all = n0 + a.side[1].n, D = a.D, pairs = a.turn.pairs;
   const Runs at = runs_of<LAYOUT>(a.turn, j);
-  v4u p[IT][2], w[IT][2];
+  const float inv = 1.0f / (float)D;
+  const bool norms = !BACK && (a.side[0].w || a.side[1].w);
+  v4u w[2][2];   // this lane's weights of both sides
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int hh = head0 + i * per;
-    const bool k = hh >= n0;
-    const auto& sd = a.side[k];
-    const uint16_t* x = BACK ? sd.dy + tok * sd.dy_ts + (hh - (k ? n0 : 0)) * sd.dy_hs
-                             : sd.x + tok * sd.x_ts + (hh - (k ? n0 : 0)) * sd.x_hs;
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      p[i][r] = w[i][r] = v4u{0, 0, 0, 0};
-      if (hh < all && at.at[r] < D) {
-        p[i][r] = *reinterpret_cast<const v4u*>(x + at.at[r]);
-        if (!BACK && sd.w) w[i][r] = *reinterpret_cast<const v4u*>(sd.w + at.at[r]);
-      }
+      w[k][r] = v4u{0, 0, 0, 0};
+      if (!BACK && a.side[k].w && at.at[r] < D)
+        w[k][r] = *reinterpret_cast<const v4u*>(a.side[k].w + at.at[r]);
     }
-  }
-  Angles<LAYOUT> angles;
-  angles.of(a.turn, j, pos, BACK);
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int hh = head0 + i * per;
+  auto load = [&](int i, int g, v4u (&p)[2]) {
+    const int hh = (g0 + g) * per + sub;
     const bool k = hh >= n0;
     const auto& sd = a.side[k];
+    const int64_t h = hh - (k ? n0 : 0);
+    const uint16_t* x = BACK ? sd.dy + (tok0 + i) * sd.dy_ts + h * sd.dy_hs
+                             : sd.x + (tok0 + i) * sd.x_ts + h * sd.x_hs;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      p[r] = v4u{0, 0, 0, 0};
+      if (hh < all && at.at[r] < D) p[r] = *reinterpret_cast<const v4u*>(x + at.at[r]);
+    }
+  };
+  // this wave's token and group: the wave'th of them in order, then every NW'th
+  int i = 0, g = wave;
+  auto settle = [&](int& i, int& g) {
+    for (; g >= ng; g -= ng) ++i;
+  };
+  settle(i, g);
+  v4u p[2], next[2];
+  if (i < n_tok) load(i, g, p);
+  for (int q = t; q < n_tok * pairs; q += 64 * NW) {
+    const int i = q / pairs;
+    s_cs[q] = angle(pos(i), a.turn.freqs[q - i * pairs], a.turn.factor);
+  }
+  __syncthreads();
+  while (i < n_tok) {
+    int i1 = i, g1 = g + NW;
+    settle(i1, g1);
+    if (i1 < n_tok) load(i1, g1, next);
+    const int hh = (g0 + g) * per + sub;
+    const bool k = hh >= n0;
+    const auto& sd = a.side[k];
+    Angles<LAYOUT> angles;
+    angles.of(a.turn, j, BACK, [&](int e) { return s_cs[i * pairs + e]; });
     float x[16];
-    unpack<BF>(p[i], x);
-    if (!BACK && (a.side[0].w || a.side[1].w)) {
-      const Rms m = rms_of<BF>(x, D, lanes, a.eps);
-      if (sd.w) normed<BF>(x, w[i], m);
+    unpack<BF>(p, x);
+    if (norms) {
+      const Rms m = rms_of<BF>(x, inv, lanes, a.eps);
+      if (sd.w) {
+        float wf[16];
+        const v4u wk[2] = {k ? w[1][0] : w[0][0], k ? w[1][1] : w[0][1]};
+        unpack<BF>(wk, wf);
+        over_rms(x, m);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= wf[e];
+      }
     }
     turn<LAYOUT>(x, angles, a.turn, j, row, lane);
-    pack<BF>(x, p[i]);
-    uint16_t* y = sd.y + tok * sd.y_ts + (hh - (k ? n0 : 0)) * sd.y_hs;
+    pack<BF>(x, p);
+    uint16_t* y = sd.y + (tok0 + i) * sd.y_ts + (int64_t)(hh - (k ? n0 : 0)) * sd.y_hs;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (hh < all && at.at[r] < D) *reinterpret_cast<v4u*>(y + at.at[r]) = p[i][r];
+    for (int r = 0; r < 2; ++r) {
+      if (hh < all && at.at[r] < D) *reinterpret_cast<v4u*>(y + at.at[r]) = p[r];
+      p[r] = next[r];
+    }
+    i = i1;
+    g = g1;
   }
 }
 

@@ -12,81 +12,113 @@ namespace i8l {
 
 constexpr int kRotThreads = 256, kRotWaves = kRotThreads / 64;
 
-template <bool BF, int LAYOUT, int IT, bool BACK>
-__global__ __launch_bounds__(kRotThreads) void rotate_heads_kernel(HeadArgs a, int lanes, int groups) {
+template <bool BF, int LAYOUT, bool BACK>
+__global__ __launch_bounds__(kRotThreads) void rotate_heads_kernel(HeadArgs a, int lanes, int n_tok,
+                                                                   int groups, int per_wg) {
+  __shared__ float2 s_cs[kTurnTokens * kMaxPairs];
   __shared__ float s_turn[LAYOUT == kTurnOdd ? kRotWaves * kTurnRow : 1];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t task = (int64_t)blockIdx.x * kRotWaves + wave;
-  const int tok = (int)(task / groups);
-  if (tok >= a.rows) return;
-  turn_heads<BF, LAYOUT, IT, BACK>(a, tok, a.positions[tok], (int)(task % groups), lanes,
-                                   s_turn + (LAYOUT == kTurnOdd ? wave * kTurnRow : 0), lane);
+  const int64_t tok0 = (int64_t)blockIdx.x * n_tok;
+  const int g0 = blockIdx.y * per_wg;
+  const int32_t* pos = a.positions + tok0;
+  turn_heads<BF, LAYOUT, kRotWaves, BACK>(
+      a, tok0, (int)min((int64_t)n_tok, a.rows - tok0), [&](int i) { return pos[i]; }, g0,
+      min(per_wg, groups - g0), lanes, s_cs,
+      s_turn + (LAYOUT == kTurnOdd ? (threadIdx.x >> 6) * kTurnRow : 0));
 }
 
-// The gradient of one side (blockIdx.y): its waves go through the side's tokens and
-// heads; each lane keeps the sums of its 16 elements of dw, which meet in the
-// workgroup's row of `part`.
+// The gradient of one side (blockIdx.y): a workgroup takes n_tok tokens at a time, a wave
+// a token's group of heads; each lane keeps the sums of its 16 elements of dw, which meet
+// in the workgroup's row of `part`.
 template <bool BF, int LAYOUT>
-__global__ __launch_bounds__(kRotThreads) void rotate_grad_kernel(HeadArgs a, int lanes) {
+__global__ __launch_bounds__(kRotThreads) void rotate_grad_kernel(HeadArgs a, int lanes, int n_tok) {
+  __shared__ float2 s_cs[kTurnTokens * kMaxPairs];
   __shared__ float s_turn[LAYOUT == kTurnOdd ? kRotWaves * kTurnRow : 1];
   __shared__ float s_dw[kRotWaves][16 * 16];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int j = lane & (lanes - 1), sub = lane / lanes, per = 64 / lanes, D = a.D, pairs = a.turn.pairs;
   const auto& sd = a.side[blockIdx.y];
-  const int per = 64 / lanes, j = lane & (lanes - 1), D = a.D;
-  const int groups = (sd.n + per - 1) / per;
   const Runs at = runs_of<LAYOUT>(a.turn, j);
-  float wf[16], dw[16];
-  {
-    v4u w[2];
+  const float inv = 1.0f / (float)D;
+  const int groups = (sd.n + per - 1) / per;
+  float* row = s_turn + (LAYOUT == kTurnOdd ? wave * kTurnRow : 0);
+  v4u w[2];
+  float dw[16];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      w[r] = v4u{0, 0, 0, 0};
-      if (sd.w && at.at[r] < D) w[r] = *reinterpret_cast<const v4u*>(sd.w + at.at[r]);
-    }
-    unpack<BF>(w, wf);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) dw[e] = 0.0f;
+  for (int r = 0; r < 2; ++r) {
+    w[r] = v4u{0, 0, 0, 0};
+    if (sd.w && at.at[r] < D) w[r] = *reinterpret_cast<const v4u*>(sd.w + at.at[r]);
   }
-  const int64_t tasks = (int64_t)a.rows * groups, step = (int64_t)gridDim.x * kRotWaves;
-  for (int64_t task = (int64_t)blockIdx.x * kRotWaves + wave; task < tasks; task += step) {
-    const int tok = (int)(task / groups), hh = (int)(task % groups) * per + lane / lanes;
-    v4u p[2], q[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      p[r] = q[r] = v4u{0, 0, 0, 0};
-      if (hh < sd.n && at.at[r] < D) {
-        p[r] = *reinterpret_cast<const v4u*>(sd.dy + tok * sd.dy_ts + hh * sd.dy_hs + at.at[r]);
-        if (sd.w) q[r] = *reinterpret_cast<const v4u*>(sd.x + tok * sd.x_ts + hh * sd.x_hs + at.at[r]);
+  for (int e = 0; e < 16; ++e) dw[e] = 0.0f;
+  for (int64_t tok0 = (int64_t)blockIdx.x * n_tok; tok0 < a.rows; tok0 += (int64_t)gridDim.x * n_tok) {
+    const int n = (int)min((int64_t)n_tok, a.rows - tok0);
+    int i = 0, g = wave;   // a wave's token and group, as in turn_heads
+    auto settle = [&](int& i, int& g) {
+      for (; g >= groups; g -= groups) ++i;
+    };
+    settle(i, g);
+    auto load = [&](int i, int g, v4u (&p)[2], v4u (&q)[2]) {
+      const int64_t hh = g * per + sub;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        p[r] = q[r] = v4u{0, 0, 0, 0};
+        if (hh < sd.n && at.at[r] < D) {
+          p[r] = *reinterpret_cast<const v4u*>(sd.dy + (tok0 + i) * sd.dy_ts + hh * sd.dy_hs + at.at[r]);
+          if (sd.w) q[r] = *reinterpret_cast<const v4u*>(sd.x + (tok0 + i) * sd.x_ts + hh * sd.x_hs + at.at[r]);
+        }
       }
+    };
+    v4u p[2], q[2], p1[2], q1[2];
+    if (i < n) load(i, g, p, q);
+    for (int c = t; c < n * pairs; c += kRotThreads) {
+      const int tok = c / pairs;
+      s_cs[c] = angle(a.positions[tok0 + tok], a.turn.freqs[c - tok * pairs], a.turn.factor);
     }
-    Angles<LAYOUT> angles;
-    angles.of(a.turn, j, a.positions[tok], true);
-    float g[16];
-    unpack<BF>(p, g);
-    turn<LAYOUT>(g, angles, a.turn, j, s_turn + (LAYOUT == kTurnOdd ? wave * kTurnRow : 0), lane);
-    if (sd.w) {   // uniform
-      float x[16];
-      unpack<BF>(q, x);
-      const Rms m = rms_of<BF>(x, D, lanes, a.eps);
-      float dot = 0.0f;
+    __syncthreads();
+    while (i < n) {
+      int i1 = i, g1 = g + kRotWaves;
+      settle(i1, g1);
+      if (i1 < n) load(i1, g1, p1, q1);
+      const int64_t hh = g * per + sub;
+      Angles<LAYOUT> angles;
+      angles.of(a.turn, j, true, [&](int e) { return s_cs[i * pairs + e]; });
+      float y[16];
+      unpack<BF>(p, y);
+      turn<LAYOUT>(y, angles, a.turn, j, row, lane);
+      if (sd.w) {   // uniform
+        float x[16], wf[16];
+        unpack<BF>(q, x);
+        unpack<BF>(w, wf);
+        const Rms m = rms_of<BF>(x, inv, lanes, a.eps);
+        over_rms(x, m);
+        float dot = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = x[e] * m.pre * m.r;      // normed
-        dw[e] = __builtin_fmaf(g[e], x[e], dw[e]);
-        g[e] *= wf[e];
-        dot = __builtin_fmaf(g[e], x[e], dot);
+        for (int e = 0; e < 16; ++e) {
+          dw[e] = __builtin_fmaf(y[e], x[e], dw[e]);
+          y[e] *= wf[e];
+          dot = __builtin_fmaf(y[e], x[e], dot);
+        }
+        dot = head_sum(dot, lanes) * inv;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = __builtin_fmaf(-x[e], dot, y[e]) * m.r;
+        if (__any(m.pre != 1.0f)) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] *= m.pre;
+        }
       }
-      dot = head_sum(dot, lanes) / (float)D;
+      pack<BF>(y, p);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) g[e] = (g[e] - x[e] * dot) * m.r * m.pre;
+      for (int r = 0; r < 2; ++r) {
+        if (hh < sd.n && at.at[r] < D)
+          *reinterpret_cast<v4u*>(sd.y + (tok0 + i) * sd.y_ts + hh * sd.y_hs + at.at[r]) = p[r];
+        p[r] = p1[r];
+        q[r] = q1[r];
+      }
+      i = i1;
+      g = g1;
     }
-    pack<BF>(g, p);
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (hh < sd.n && at.at[r] < D)
-        *reinterpret_cast<v4u*>(sd.y + tok * sd.y_ts + hh * sd.y_hs + at.at[r]) = p[r];
+    __syncthreads();   // the angles have been read
   }
   if (!sd.w) return;
 #pragma unroll
@@ -99,7 +131,7 @@ __global__ __launch_bounds__(kRotThreads) void rotate_grad_kernel(HeadArgs a, in
       for (int e = 0; e < 8; ++e)
         if (at.at[r] < D) s_dw[wave][at.at[r] + e] = dw[8 * r + e];
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += kRotThreads) {
+  for (int d = t; d < D; d += kRotThreads) {
     float v = 0.0f;
 #pragma unroll
     for (int i = 0; i < kRotWaves; ++i) v += s_dw[i][d];
@@ -117,6 +149,7 @@ __global__ __launch_bounds__(1024) void rotate_dw_kernel(HeadArgs a, int n) {
   const int c = threadIdx.x & 15, row = threadIdx.x >> 4, d = blockIdx.x * 16 + c;
   const float* p = a.part + (size_t)blockIdx.y * n * a.D + d;
   float v = 0.0f;
+#pragma unroll 4
   for (int i = row; i < n; i += 64) v += p[(size_t)i * a.D];
   s[row][c] = v;
   __syncthreads();
@@ -129,31 +162,23 @@ __global__ __launch_bounds__(1024) void rotate_dw_kernel(HeadArgs a, int n) {
 
 namespace {
 
-// Groups of heads that a wave takes one after another (kIt) and waves a token.
+// Four tokens a workgroup where there are workgroups enough: their angles are then formed
+// once, one or two a thread.  Otherwise one, and a group of heads a wave.
 template <bool BF, int LAYOUT, bool BACK>
 void launch_rows(const HeadArgs& a, hipStream_t stream) {
   const int lanes = lanes_of(a.D), per = 64 / lanes;
   const int groups = (a.side[0].n + a.side[1].n + per - 1) / per;
-  // Up to four groups a wave where there are waves enough without.
-  int it = (int64_t)a.rows * groups >= 16384 ? 4 : 1;
-  const int waves = (groups + it - 1) / it;
-  it = (groups + waves - 1) / waves;
-  const int64_t blocks = ((int64_t)a.rows * waves + kRotWaves - 1) / kRotWaves;
-#define I8L_ROT(IT)                                                                         \
-  hipLaunchKernelGGL((rotate_heads_kernel<BF, LAYOUT, IT, BACK>), dim3((uint32_t)blocks),   \
-                     dim3(kRotThreads), 0, stream, a, lanes, waves)
-  if (it == 1) I8L_ROT(1);
-  else if (it == 2) I8L_ROT(2);
-  else if (it == 3) I8L_ROT(3);
-  else I8L_ROT(4);
-#undef I8L_ROT
+  const int n_tok = a.rows >= 2048 ? kTurnTokens : 1;
+  const int per_wg = n_tok == 1 && groups > kRotWaves && (int64_t)a.rows * groups < 8192 ? kRotWaves : groups;
+  hipLaunchKernelGGL((rotate_heads_kernel<BF, LAYOUT, BACK>),
+                     dim3((a.rows + n_tok - 1) / n_tok, (groups + per_wg - 1) / per_wg),
+                     dim3(kRotThreads), 0, stream, a, lanes, n_tok, groups, per_wg);
 }
 
-int grad_blocks(int rows, int heads, int D) {
-  const int per = 64 / lanes_of(D);
-  const int64_t tasks = (int64_t)rows * ((heads + per - 1) / per);
-  const int64_t blocks = (tasks + 2 * kRotWaves - 1) / (2 * kRotWaves);
-  return (int)(blocks < 1 ? 1 : blocks > 1024 ? 1024 : blocks);
+int grad_tokens(int rows) { return rows >= 4096 ? kTurnTokens : 1; }
+int grad_blocks(int rows) {
+  const int n = grad_tokens(rows), blocks = (int)(((int64_t)rows + n - 1) / n);
+  return blocks < 1 ? 1 : blocks > 1024 ? 1024 : blocks;
 }
 
 template <bool BF, int LAYOUT>
@@ -162,10 +187,9 @@ void launch_grad(const HeadArgs& a, hipStream_t stream) {
     launch_rows<BF, LAYOUT, true>(a, stream);
     return;
   }
-  const int sides = a.side[1].n ? 2 : 1;
-  const int blocks = grad_blocks(a.rows, a.side[0].n, a.D);
-  hipLaunchKernelGGL((rotate_grad_kernel<BF, LAYOUT>), dim3(blocks, sides), dim3(kRotThreads), 0,
-                     stream, a, lanes_of(a.D));
+  const int sides = a.side[1].n ? 2 : 1, blocks = grad_blocks(a.rows);
+  hipLaunchKernelGGL((rotate_grad_kernel<BF, LAYOUT>), dim3(blocks, sides), dim3(kRotThreads), 0, stream, a,
+                     lanes_of(a.D), grad_tokens(a.rows));
   hipLaunchKernelGGL((rotate_dw_kernel<BF>), dim3(a.D / 16, sides), dim3(1024), 0, stream, a, blocks);
 }
 
@@ -190,9 +214,7 @@ hipError_t launch_rotate_heads(const HeadArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-size_t head_partials(int rows, int heads, int D) {
-  return 2 * (size_t)grad_blocks(rows, heads, D) * D;
-}
+size_t head_partials(int rows, int D) { return 2 * (size_t)grad_blocks(rows) * D; }
 
 hipError_t launch_rotate_heads_backward(const HeadArgs& a, hipStream_t stream) {
   I8L_TURN(launch_grad);

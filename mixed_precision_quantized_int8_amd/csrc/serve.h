@@ -100,7 +100,7 @@ struct HeadArgs {
 };
 hipError_t launch_rotate_heads(const HeadArgs& a, hipStream_t stream);
 // Floats of partial sums that the backward pass needs (0: neither side has a weight).
-size_t head_partials(int rows, int heads, int D);
+size_t head_partials(int rows, int D);
 hipError_t launch_rotate_heads_backward(const HeadArgs& a, hipStream_t stream);
 
 // kv rows: element (t, h, d) at t * ts + h * hs + d.

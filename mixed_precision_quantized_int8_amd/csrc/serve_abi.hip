@@ -449,12 +449,11 @@ I8L_API i8l_status int8_rotate_heads(const i8l_heads* q, const i8l_heads* k, int
   return hip_status(fn, i8l::launch_rotate_heads(a, static_cast<hipStream_t>(stream)));
 }
 
-I8L_API size_t i8l_rotate_heads_workspace_bytes(int64_t rows, int64_t q_heads, int32_t head_dim) {
+I8L_API size_t i8l_rotate_heads_workspace_bytes(int64_t rows, int32_t head_dim) {
   const char* fn = "i8l_rotate_heads_workspace_bytes";
-  if (check_head_dim(fn, head_dim) != I8L_OK || check_count(fn, "rows", rows, 0, INT32_MAX) != I8L_OK ||
-      check_count(fn, "q_heads", q_heads, 1, 65536) != I8L_OK)
+  if (check_head_dim(fn, head_dim) != I8L_OK || check_count(fn, "rows", rows, 0, INT32_MAX) != I8L_OK)
     return 0;
-  return sizeof(float) * i8l::head_partials((int)rows, (int)q_heads, head_dim);
+  return sizeof(float) * i8l::head_partials((int)rows, head_dim);
 }
 
 I8L_API i8l_status int8_rotate_heads_backward(const i8l_heads_grad* q, const i8l_heads_grad* k,
@@ -477,7 +476,7 @@ I8L_API i8l_status int8_rotate_heads_backward(const i8l_heads_grad* q, const i8l
   if (rows == 0 && !weights) return ok();
   if (rows) CHECK_PTR(positions, 4);
   if (weights) {
-    const size_t need = sizeof(float) * i8l::head_partials((int)rows, a.side[0].n, head_dim);
+    const size_t need = sizeof(float) * i8l::head_partials((int)rows, head_dim);
     CHECK_PTR(workspace, 16);
     if (workspace_bytes < need)
       return fail(I8L_ERR_WORKSPACE, fn, "workspace has %zu bytes, %zu required", workspace_bytes,

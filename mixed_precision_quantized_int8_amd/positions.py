@@ -211,7 +211,7 @@ def rotate_heads_backward(dq, positions, rotary=None, q=None, dk=None, k=None, q
         raise ValueError("k_weight or dk_out without dk")
     need = 0
     if workspace is None and (dqw is not None or dkw is not None):
-        need = rotate_heads_workspace_bytes(rows, H, D)
+        need = rotate_heads_workspace_bytes(rows, D)
     hold, ws, nb = _scratch(workspace, need, dev)
     with _on(dev):
         check(lib().int8_rotate_heads_backward(
@@ -221,9 +221,9 @@ def rotate_heads_backward(dq, positions, rotary=None, q=None, dk=None, k=None, q
     return dq_out, dk_out, dqw, dkw
 
 
-def rotate_heads_workspace_bytes(rows, q_heads, head_dim):
+def rotate_heads_workspace_bytes(rows, head_dim):
     """Bytes of scratch that ``rotate_heads_backward`` uses where there is a weight."""
-    return int(lib().i8l_rotate_heads_workspace_bytes(rows, q_heads, head_dim))
+    return int(lib().i8l_rotate_heads_workspace_bytes(rows, head_dim))
 
 
 def cache_append(cache, k, v, page_table, lengths, q=None, rotary=None, q_weight=None, k_weight=None,

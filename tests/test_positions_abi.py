@@ -74,7 +74,7 @@ def test_rotate_heads_refusals(i8l):
 
 def test_rotate_heads_backward_refusals(i8l):
     L = i8l.lib()
-    need = L.i8l_rotate_heads_workspace_bytes(100, 4, 64)
+    need = L.i8l_rotate_heads_workspace_bytes(100, 64)
     assert need > 0
 
     def call(q=None, k=None, D=64, rows=100, pos=P16, rot=None, eps=1e-6, dtype=0, ws=P16, n=need):
@@ -96,8 +96,8 @@ def test_rotate_heads_backward_refusals(i8l):
                                         None) == INVALID
     # without weights: no input, no workspace; without rows nothing to do
     assert call(q=grad_struct(weight=None, dweight=None, x=None), rows=0, ws=None, n=0) == OK
-    assert L.i8l_rotate_heads_workspace_bytes(100, 4, 24) == 0
-    assert L.i8l_rotate_heads_workspace_bytes(-1, 4, 64) == 0
+    assert L.i8l_rotate_heads_workspace_bytes(100, 24) == 0
+    assert L.i8l_rotate_heads_workspace_bytes(-1, 64) == 0
 
 
 def test_cache_append_refusals(i8l):
