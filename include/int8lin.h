@@ -528,6 +528,11 @@ i8l_status int8_tree_plan(const int32_t *parents, const int32_t *lengths, const 
                           int64_t n, int64_t rows, int64_t max_q, int32_t *positions,
                           uint64_t *masks, int32_t words, void *stream);
 
+/* Workspace bytes of int8_tree_attention for these sizes (0: none needed, or sizes that
+ * the call refuses). */
+size_t i8l_tree_workspace_bytes(const i8l_kv_cache *cache, int64_t n, int64_t q_heads,
+                                int64_t max_q, int64_t max_len, int64_t window);
+
 /* Attention of drafts over the cache, which does not hold them, and over each other: a
  * draft's query at position p sees the cached tokens t with p - t < window (window 0:
  * all), and the drafts of its sequence that its mask names, with the same window on
@@ -541,7 +546,7 @@ i8l_status int8_tree_plan(const int32_t *parents, const int32_t *lengths, const 
  *   positions  int32 [rows]; may be NULL without window and alibi
  *   max_q      at least the drafts of any one sequence (those past it are neither seen
  *              nor answered), at most 64 * words
- *   workspace  i8l_attention_workspace_bytes(cache, n, q_heads, max_q, max_len, window)
+ *   workspace  i8l_tree_workspace_bytes(...) bytes, 16-byte aligned
  * Everything else as for int8_cache_attention. */
 i8l_status int8_tree_attention(const i8l_kv_cache *cache, const i8l_sequences *seqs,
                                const uint16_t *q, int64_t q_token_stride, int64_t q_head_stride,

@@ -54,6 +54,7 @@ __all__ = [
     "cache_append",
     "tree_plan",
     "tree_attention",
+    "tree_workspace_bytes",
     "tree_accept",
     "workspace_layout",
     "workspace_bytes",
@@ -69,7 +70,7 @@ _SERVING = ("rmsnorm_quant", "linear_codes", "KVCache", "new_cache", "cache_writ
 
 _POSITIONS = ("Rotary", "rotary", "rotate_heads", "rotate_heads_backward",
               "rotate_heads_workspace_bytes", "cache_append", "tree_plan", "tree_attention",
-              "tree_accept")
+              "tree_workspace_bytes", "tree_accept")
 
 
 def __getattr__(name):

@@ -52,6 +52,7 @@ EXPORTS = (
     "int8_rotate_heads_backward",
     "int8_cache_append",
     "int8_tree_plan",
+    "i8l_tree_workspace_bytes",
     "int8_tree_attention",
     "int8_tree_accept",
     "i8l_last_error",
@@ -233,6 +234,8 @@ def lib() -> ctypes.CDLL:
     L.int8_cache_append.restype = ctypes.c_int
     L.int8_tree_plan.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, i32, vp]
     L.int8_tree_plan.restype = ctypes.c_int
+    L.i8l_tree_workspace_bytes.argtypes = [cache, i64, i64, i64, i64, i64]
+    L.i8l_tree_workspace_bytes.restype = sz
     L.int8_tree_attention.argtypes = [cache, seqs, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, i64,
                                       i64, i64, vp, i32, vp, f32, i64, vp, vp, vp, sz, vp]
     L.int8_tree_attention.restype = ctypes.c_int

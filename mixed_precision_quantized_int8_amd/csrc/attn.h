@@ -99,6 +99,84 @@ __device__ __forceinline__ void say_empty(const AttnArgs& a, int b, int h, int r
   a.part[2 * at + 1] = 0.0f;
 }
 
+// How a call with trees is shared out where lengths and drafts are ragged (they are known
+// on the device only, and splits that suit the longest sequence leave most compute
+// units waiting for it).  Each tile of rows of a sequence counts its blocks of 128 keys, and
+// kShareCost more for its start and its drafts; the blocks of all tiles stand in one line,
+// and workgroup s of a head takes those from s * each on, a segment of a tile at a time.
+// So at most its first segment lacks the tile's start and at most its last the end: two
+// places for partial results a workgroup.  Lane b plans sequence b (at most 64).
+struct SharePlan {
+  int first, tiles, blocks;   // where the sequence's blocks begin; of a tile
+};
+struct Segment {
+  int b, tile, begin, end;    // keys
+  bool last;                  // the drafts are its too
+  int part;                   // place of its partial results, -1: it is the whole tile
+  int next;                   // block that the next one begins at
+};
+constexpr int kShareSeqs = 64, kShareCost = 2;
+constexpr int kShareHead = 2 * kShareSeqs + 64;   // words before the partial results, for the join
+// Inclusive sum over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v) {
+#define I8L_SCAN(ctrl, rows) v += __builtin_amdgcn_update_dpp(0, v, ctrl, rows, 0xf, false)
+  I8L_SCAN(0x111, 0xf);   // by 1, 2, 4, 8 within 16
+  I8L_SCAN(0x112, 0xf);
+  I8L_SCAN(0x114, 0xf);
+  I8L_SCAN(0x118, 0xf);
+  I8L_SCAN(0x142, 0xa);   // lane 15 to 16 .. 31, 47 to 48 .. 63
+  I8L_SCAN(0x143, 0xc);   // lane 31 to 32 .. 63
+#undef I8L_SCAN
+  return v;
+}
+// The first wave's: its lane's plan, and in *each and *total the blocks of a workgroup and
+// of all.
+__device__ __forceinline__ SharePlan plan_shares(const TreeArgs& a, int rows, int* each, int* total) {
+  const int lane = threadIdx.x & 63;
+  SharePlan p{0, 0, 0};
+  if (lane < a.s.B) {
+    const Rows r = rows_of(a, lane);
+    p.tiles = (r.n * a.G + rows - 1) / rows;
+    p.blocks = (r.len + 127) / 128;
+  }
+  const int mine = p.tiles * (p.blocks + kShareCost), upto = wave_scan(mine);
+  p.first = upto - mine;
+  const int all = __builtin_amdgcn_readlane(upto, 63), share = (all + a.shares - 1) / a.shares;
+  *each = max(share, 1);
+  *total = all;
+  if (blockIdx.x == 0) {
+    int32_t* table = reinterpret_cast<int32_t*>(a.part);
+    table[lane] = p.first;
+    table[kShareSeqs + lane] = p.blocks;
+    if (lane == 0) table[2 * kShareSeqs] = max(share, 1);
+  }
+  return p;
+}
+// The segment that begins at block x of the line (x < total); to: the workgroup's end.
+__device__ __forceinline__ Segment segment_at(const SharePlan& p, int x, int to, int s) {
+  const int b = __builtin_ctzll(__ballot(p.first + p.tiles * (p.blocks + kShareCost) > x));
+  const int blocks = __builtin_amdgcn_readlane(p.blocks, b), c = blocks + kShareCost;
+  const int v = x - __builtin_amdgcn_readlane(p.first, b);
+  Segment r;
+  r.b = b;
+  r.tile = v / c;
+  const int off = v - r.tile * c, stop = min(c, off + to - x);
+  r.begin = 128 * off;
+  r.end = 128 * min(stop, blocks);
+  r.last = stop == c;
+  r.part = off == 0 && r.last ? -1 : 2 * s + (off == 0);
+  r.next = x + stop - off;
+  return r;
+}
+// (m, l) and output of row r of the tile of partial results `part`.
+__device__ __forceinline__ size_t share_row(const TreeArgs& a, int part, int h, int rows, int r) {
+  return ((size_t)part * a.c.H + h) * rows + r;
+}
+__device__ __forceinline__ float* share_ml(const TreeArgs& a, size_t at) { return a.part + kShareHead + 2 * at; }
+__device__ __forceinline__ float* share_out(const TreeArgs& a, int rows, size_t at) {
+  return a.part + kShareHead + 4 * (size_t)a.shares * a.c.H * rows + at * a.c.D;
+}
+
 // 16 rows (queries of one kv head: token-major, the G heads of a token together)
 // against a range of keys.  S^T = K . Q^T and O^T = V^T . P^T on 16x16x32
 // matrix instructions; lane l holds query l & 15, and of a tile of 64 keys the
@@ -596,8 +674,13 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
 constexpr int kApTile = 64;
 constexpr float kApSlack = 8.0f;
 
-template <bool BF, int DP, int NW, bool ALIBI, bool TREE>
-__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(ArgsOf<TREE> a) {
+//
+// attn_run: the workgroup's rows r_wg .. of kv head h of sequence b, and its split of the
+// keys; SHARE: the segment's keys, without a window.
+template <bool BF, int DP, int NW, bool ALIBI, bool TREE, bool SHARE>
+__device__ __forceinline__ void attn_run(const ArgsOf<TREE>& a, int b, int h, int r_wg, int split,
+                                         const Segment& seg) {
+  const int n_split = SHARE ? 1 : a.n_split, chunk = a.chunk;
   constexpr int NT = 64 * NW, kRows = 32 * NW;
   constexpr int NK = DP / 16;               // contraction steps of Q . K
   constexpr int ND = DP / 32;               // 32-row blocks of O^T
@@ -615,16 +698,14 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
   __shared__ uint32_t s_odd[2];   // a tile of the incomplete page holds infinities or NaNs
   __shared__ int s_low[TREE ? NW : 1], s_pos[TREE ? kApTile : 1];
 
-  const int t = threadIdx.x, lane = t & 63;
+  int t = threadIdx.x;
+  if (SHARE) asm volatile("" : "+v"(t), "+s"(h));   // (nothing of a segment is formed before it)
+  const int lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int l32 = lane & 31, hf = lane >> 5;
   const int H = a.c.H, D = a.c.D, ps = a.c.ps, P = 1 << ps, G = a.G;
-  const int b = blockIdx.z, split = blockIdx.y, h = blockIdx.x % H;
   const Rows sq = rows_of(a, b);
   const int n_rows = sq.n * G;
-  // the last rows see the most keys: they go first
-  const int tiles = (int)gridDim.x / H;
-  const int r_wg = (tiles - 1 - (int)blockIdx.x / H) * kRows;
   if (r_wg >= n_rows) return;
   const int first_pos = sq.first_pos;
 
@@ -644,7 +725,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
   // what every row of the wave sees, and what some row of the workgroup does
   int wv_lo1 = low(min(r_wave + 32, n_rows) - 1), wg_lo = low(r_wg);
   const int wv_hi0 = high(min(r_wave, n_rows - 1)), wg_hi = high(min(r_wg + kRows, n_rows) - 1);
-  if (TREE && a.window > 0) {   // (rows of a tree are in any order)
+  if (TREE && !SHARE && a.window > 0) {   // (rows of a tree are in any order)
     wv_lo1 = wg_lo = lo;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -661,13 +742,24 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
 
   const int coded = sq.len >> ps << ps;
   const int first = wg_lo & ~127;
-  const int begin = first + split * a.chunk;
-  const int end = split == a.n_split - 1 ? wg_hi : min(begin + a.chunk, wg_hi);
+  const int begin = SHARE ? seg.begin : first + split * chunk;
+  const int end = SHARE ? min(seg.end, wg_hi) : split == n_split - 1 ? wg_hi : min(begin + chunk, wg_hi);
+  const bool drafts = SHARE ? seg.last : TREE && split == n_split - 1;
   // nothing to see here: no more than that is said
-  if (begin >= end && a.n_split > 1 && !(TREE && split == a.n_split - 1)) {
-    for (int r = t; r < min(kRows, n_rows - r_wg); r += NT) say_empty(a, b, h, r_wg + r, split);
+  if (begin >= end && (n_split > 1 || SHARE) && !drafts) {
+    for (int r = t; r < min(kRows, n_rows - r_wg); r += NT) {
+      if constexpr (SHARE) {
+        float* ml = share_ml(a, share_row(a, seg.part, h, kRows, r));
+        ml[0] = -__builtin_inff();
+        ml[1] = 0.0f;
+      } else {
+        say_empty(a, b, h, r_wg + r, split);
+      }
+    }
     return;
   }
+  // a wave without rows only stages (a tree's rows rarely fill the workgroup)
+  const bool idle = TREE && r_wave >= n_rows;
   const int c_begin = max(begin, wg_lo & ~(kApTile - 1));
   const int c_end = min(end, coded);
   const int n_coded = c_end > c_begin ? (c_end - c_begin + kApTile - 1) / kApTile : 0;
@@ -938,7 +1030,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
 #pragma unroll
     for (int u = 0; u < CPT; ++u) load_page(u, 2);
     lds_sync();
-    first_scores(0, 0);
+    if (!idle) first_scores(0, 0);
     for (int i = 0; i < n_coded; ++i) {
       load_meta(i);
       if (meta) {
@@ -947,7 +1039,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
         load_meta_page(i + 3);
       }
       // the staging in the first slots: convert and store step i + 1, load step i + 2
-      half_tile(i, 0, [&](int n) {
+      auto stage = [&](int n) {
         constexpr int kPer = (4 * CPT + NV - 1) / NV;   // units a slot
 #pragma unroll
         for (int x = n * kPer; x < (n + 1) * kPer; ++x) {
@@ -955,12 +1047,20 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
           else if (x < 3 * CPT) load_chunk(x - 2 * CPT, i + 2);
           else if (x < 4 * CPT) load_page(x - 3 * CPT, i + 3);
         }
-      });
+      };
+      if (idle) {
+#pragma unroll
+        for (int u = 0; u < CPT; ++u) asm volatile("" : "+v"(raw[u]));   // (converted here, not before)
+#pragma unroll
+        for (int n = 0; n < NV; ++n) stage(n);
+      } else {
+        half_tile(i, 0, stage);
+      }
       lds_sync();
       // (past the last tile the scores are of whatever the buffer holds, and unused)
-      half_tile(i, 1, [](int) {});
+      if (!idle) half_tile(i, 1, [](int) {});
     }
-    last_outputs(n_coded - 1, 1);
+    if (!idle) last_outputs(n_coded - 1, 1);
   }
   // ---- the keys of the incomplete page, 16 bits each, a tile at a time -------------
   // Infinities and NaNs among the values are cleared, since a hidden key's weight of 0
@@ -1001,6 +1101,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
     load_meta(0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+      if (idle) break;
       first_scores(0, k);
       top = -__builtin_inff();
       add[0] = add[1] = 0.0f;
@@ -1032,7 +1133,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
   // ---- the drafts, a tile at a time, in the tail's way: values are transposed on their
   // way into LDS (two drafts' 8 dimensions a thread, as 8 dwords of two drafts)
   if constexpr (TREE) {
-    const int n_drafts = split == a.n_split - 1 ? sq.n : 0;
+    const int n_drafts = drafts ? sq.n : 0;
     for (int t0 = 0; t0 < n_drafts; t0 += kApTile) {
       const int n = min(n_drafts - t0, kApTile);
       lds_sync();   // buffer 0 and s_odd have been read
@@ -1078,6 +1179,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
           if (pos - s_pos[i] >= a.window) word &= ~(1ull << i);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+        if (idle) break;
         first_scores(0, k);
         top = -__builtin_inff();
         add[0] = add[1] = 0.0f;
@@ -1116,7 +1218,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
   halves(l, &l_lo, &l_hi);
   const float sum = l_lo + l_hi;
   if (!live) return;
-  if (a.n_split == 1) {
+  if (SHARE ? seg.part < 0 : n_split == 1) {
     const int64_t row_out = (sq.c0 + qi) * H * G + h * G + qg;
     const float f = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key at all: 0
 #pragma unroll
@@ -1133,20 +1235,121 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(Arg
       }
     return;
   }
-  const size_t at = part_at(a, b, h, rr, split);
+  float *po, *ml;
+  if constexpr (SHARE) {
+    const size_t at = share_row(a, seg.part, h, kRows, rr - r_wg);
+    po = share_out(a, kRows, at);
+    ml = share_ml(a, at);
+  } else {
+    const size_t at = part_at(a, b, h, rr, split);
+    po = part_out(a, at);
+    ml = a.part + 2 * at;
+  }
 #pragma unroll
   for (int d = 0; d < ND; ++d)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int e = 32 * d + 8 * q + 4 * hf;
       if (e < D)
-        *reinterpret_cast<v4f*>(part_out(a, at) + e) =
+        *reinterpret_cast<v4f*>(po + e) =
             v4f{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
     }
   if (hf == 0) {
-    a.part[2 * at] = limit < 0.0f ? -__builtin_inff() : m;
-    a.part[2 * at + 1] = sum;
+    ml[0] = limit < 0.0f ? -__builtin_inff() : m;
+    ml[1] = sum;
   }
+}
+
+template <bool BF, int DP, int NW, bool ALIBI, bool TREE>
+__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_run_kernel(ArgsOf<TREE> a) {
+  // the last rows see the most keys: they go first
+  const int H = a.c.H, r_wg = ((int)gridDim.x / H - 1 - (int)blockIdx.x / H) * 32 * NW;
+  attn_run<BF, DP, NW, ALIBI, TREE, false>(a, blockIdx.z, blockIdx.x % H, r_wg, blockIdx.y, Segment{});
+}
+
+template <bool BF, int DP, bool ALIBI>
+__global__ __launch_bounds__(512, 2) void attn_share_kernel(TreeArgs a) {
+  __shared__ SharePlan s_plan[kShareSeqs];
+  __shared__ int s_each, s_total;
+  const int H = a.c.H, s = blockIdx.x / H;
+  if (threadIdx.x < 64) {
+    int each, total;
+    s_plan[threadIdx.x] = plan_shares(a, 256, &each, &total);
+    if (threadIdx.x == 0) {
+      s_each = each;
+      s_total = total;
+    }
+  }
+  __syncthreads();
+  const int to = __builtin_amdgcn_readfirstlane(min((s + 1) * s_each, s_total));
+  for (int x = __builtin_amdgcn_readfirstlane(s * s_each); x < to;) {
+    const Segment g = segment_at(s_plan[threadIdx.x & 63], x, to, s);
+    attn_run<BF, DP, 8, ALIBI, true, true>(a, g.b, blockIdx.x % H, 256 * g.tile, 0, g);
+    x = g.next;
+    __syncthreads();   // the segment's tiles have been read
+  }
+}
+
+// The segments of one row together, where its tile has more than one: `lanes` neighbouring
+// lanes a row (a power of two, four elements each), lane s of them weighs segment s; the
+// outputs of eight segments are on their way at a time.
+template <bool BF>
+__global__ __launch_bounds__(256) void share_join_kernel(TreeArgs a, int lanes) {
+  constexpr int rows = 256;
+  const int D = a.c.D, H = a.c.H, G = a.G, b = blockIdx.z, h = blockIdx.y;
+  const int t = threadIdx.x, mine = t & (lanes - 1), d = 4 * mine;
+  const int R = (int)blockIdx.x * (256 / lanes) + t / lanes;
+  const int32_t* table = reinterpret_cast<const int32_t*>(a.part);
+  const Rows sq = rows_of(a, b);
+  const int n_rows = sq.n * G;
+  if ((int)blockIdx.x * (256 / lanes) >= n_rows) return;   // uniform
+  const int r = min(R, n_rows - 1), tile = r / rows;
+  const int each = table[2 * kShareSeqs], c = table[kShareSeqs + b] + kShareCost, x0 = table[b] + tile * c;
+  const int s_first = x0 / each, n = (x0 + c - 1) / each - s_first + 1;
+  if (n < 2) return;   // (a workgroup's rows are of one tile: 256 / lanes divides 256)
+  // segment i: of workgroup s_first + i, the first in its place 1, the others in place 0
+  auto row_of_part = [&](int i) { return share_row(a, 2 * (s_first + i) + (i == 0), h, rows, r - tile * rows); };
+  float m = -__builtin_inff();
+  for (int s = mine; s < n; s += lanes) m = __builtin_fmaxf(m, share_ml(a, row_of_part(s))[0]);
+  for (int off = 1; off < lanes; off <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, off, 64));
+  const float ms = m == -__builtin_inff() ? 0.0f : m;
+  float l = 0.0f;
+  v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < n; s0 += lanes) {
+    float f = 0.0f, ls = 0.0f;
+    if (s0 + mine < n) {
+      const float* ml = share_ml(a, row_of_part(s0 + mine));
+      f = __builtin_amdgcn_exp2f(ml[0] - ms);
+      ls = ml[1];
+      l = __builtin_fmaf(ls, f, l);
+    }
+    const int left = min(lanes, n - s0);
+    for (int j = 0; j < left; j += 8) {
+      float fj[8];
+      v4f x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int from = (t & 63 & ~(lanes - 1)) + min(j + e, lanes - 1);
+        fj[e] = __shfl(f, from, 64);
+        // an empty segment has no output; one whose weight underflows counts, by an infinity in it
+        const bool some = j + e < left && __shfl(ls, from, 64) != 0.0f;
+        x[e] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (some && d < D)
+          x[e] = *reinterpret_cast<const v4f*>(share_out(a, rows, row_of_part(s0 + j + e)) + d);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[e][i], fj[e], o[i]);
+    }
+  }
+  for (int off = 1; off < lanes; off <<= 1) l += __shfl_xor(l, off, 64);
+  if (R >= n_rows || d >= D) return;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint2 w;
+  w.x = pack2<BF>(o[0] * inv, o[1] * inv);
+  w.y = pack2<BF>(o[2] * inv, o[3] * inv);
+  *reinterpret_cast<uint2*>(a.out + ((sq.c0 + R / G) * H * G + h * G + R % G) * (int64_t)D + d) = w;
 }
 
 // The splits of one row together: one wave per row.  Lane s weighs split s; the
@@ -1253,6 +1456,13 @@ template <bool BF, bool ALIBI, bool TREE>
 void launch_kernel(const ArgsOf<TREE>& a, const Plan& p, hipStream_t stream) {
   const int D = a.c.D;
   const dim3 grid(a.c.H * ((a.G * a.max_q + p.rows - 1) / p.rows), a.n_split, a.s.B);
+  if constexpr (TREE)
+    if (a.shares) {
+      const dim3 all(a.c.H * a.shares);
+      if (D <= 64) hipLaunchKernelGGL((attn_share_kernel<BF, 64, ALIBI>), all, dim3(512), 0, stream, a);
+      else hipLaunchKernelGGL((attn_share_kernel<BF, 128, ALIBI>), all, dim3(512), 0, stream, a);
+      return;
+    }
   if (p.rows == 16) {
     const dim3 block(kAdThreads);
     if (D <= 64) hipLaunchKernelGGL((attn_decode_kernel<BF, 64, ALIBI, TREE>), grid, block, 0, stream, a);
@@ -1277,10 +1487,30 @@ hipError_t launch_typed(const ArgsOf<TREE>& a, const Plan& p, hipStream_t stream
   if (a.alibi) launch_kernel<BF, true, TREE>(a, p, stream);
   else launch_kernel<BF, false, TREE>(a, p, stream);
   const hipError_t e = hipGetLastError();
+  if constexpr (TREE)
+    if (e == hipSuccess && a.shares) {
+      int lanes = 4;
+      while (4 * lanes < a.c.D) lanes *= 2;
+      const int per = 256 / lanes;
+      hipLaunchKernelGGL((share_join_kernel<BF>), dim3((a.G * a.max_q + per - 1) / per, a.c.H, a.s.B),
+                         dim3(256), 0, stream, a, lanes);
+      return hipGetLastError();
+    }
   if (e != hipSuccess || a.n_split == 1) return e;
   hipLaunchKernelGGL((attn_join_kernel<BF>), dim3((a.G * a.max_q + 3) / 4, a.c.H, a.s.B),
                      dim3(256), 0, stream, static_cast<const AttnArgs&>(a));
   return hipGetLastError();
+}
+
+// Workgroups a head that a call with trees is shared out to (0: the splits above): one a
+// compute unit.  Only where sequences are many and long enough for their lengths to matter;
+// a window bounds them, a plan has room for 64 sequences, and 128 tiles keep the number
+// of blocks (of at most 2^30 keys each) in 32 bits.
+int tree_shares(const Plan& p, int B, int H, int G, int max_q, int max_len, int window) {
+  return p.rows == 256 && B > 1 && B <= kShareSeqs && B * (((int64_t)G * max_q + 255) / 256) <= 128 &&
+                 window == 0 && max_len > 2048 && H <= 128
+             ? 256 / H
+             : 0;
 }
 
 // Chooses the kernel and the split, and launches.
@@ -1289,6 +1519,7 @@ hipError_t launch_planned(ArgsOf<TREE> a, hipStream_t stream) {
   const Plan p = plan(a.s.B, a.c.H, a.G, a.c.D, a.max_q, a.max_len, a.window);
   a.chunk = p.chunk;
   a.n_split = p.n_split;
+  if constexpr (TREE) a.shares = tree_shares(p, a.s.B, a.c.H, a.G, a.max_q, a.max_len, a.window);
   return a.c.bf16 ? launch_typed<true, TREE>(a, p, stream) : launch_typed<false, TREE>(a, p, stream);
 }
 

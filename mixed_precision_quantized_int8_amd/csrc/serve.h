@@ -147,7 +147,10 @@ struct TreeArgs : AttnArgs {
   const int32_t* positions;   // [rows], or NULL without a window and a bias
   const uint16_t *dk, *dv;    // the drafts' keys and values: element (t, h, d) at
   int64_t dk_ts, dk_hs, dv_ts, dv_hs;   // t * ts + h * hs + d
+  // set by the launcher
+  int shares;           // workgroups a head that the keys are shared out to, or 0
 };
+size_t tree_partials(int B, int H, int G, int D, int max_q, int max_len, int window);
 hipError_t launch_tree_attention(const TreeArgs& a, hipStream_t stream);
 
 // A tree of drafts from their parents, and its accepted path (tree.hip).

@@ -575,6 +575,20 @@ I8L_API i8l_status int8_tree_plan(const int32_t* parents, const int32_t* lengths
                                               static_cast<hipStream_t>(stream)));
 }
 
+I8L_API size_t i8l_tree_workspace_bytes(const i8l_kv_cache* cache, int64_t n, int64_t q_heads,
+                                        int64_t max_q, int64_t max_len, int64_t window) {
+  const char* fn = "i8l_tree_workspace_bytes";
+  i8l::Cache c;
+  if (check_cache(fn, cache, &c) != I8L_OK || check_count(fn, "n", n, 0, 65535) != I8L_OK ||
+      check_attention(fn, c, q_heads, max_q, max_len, window) != I8L_OK ||
+      check_count(fn, "max_q", max_q, 1, i8l::kMaxDrafts) != I8L_OK)
+    return 0;
+  if (n == 0) return 0;
+  window = std::min(window, kMaxTokens);
+  return sizeof(float) * i8l::tree_partials((int)n, c.H, (int)(q_heads / c.H), c.D, (int)max_q,
+                                            (int)max_len, (int)window);
+}
+
 I8L_API i8l_status int8_tree_attention(
     const i8l_kv_cache* cache, const i8l_sequences* seqs, const uint16_t* q, int64_t q_token_stride,
     int64_t q_head_stride, int64_t q_heads, const uint16_t* k, int64_t k_token_stride,
@@ -604,8 +618,8 @@ I8L_API i8l_status int8_tree_attention(
   if (positions || alibi || window) CHECK_PTR(positions, 4);
   window = std::min(window, kMaxTokens);
   const int G = (int)(q_heads / c.H);
-  const size_t need = sizeof(float) * i8l::attention_partials(s.B, c.H, G, c.D, (int)max_q,
-                                                              (int)max_len, (int)window);
+  const size_t need = sizeof(float) * i8l::tree_partials(s.B, c.H, G, c.D, (int)max_q, (int)max_len,
+                                                         (int)window);
   if (need) {
     CHECK_PTR(workspace, 16);
     if (workspace_bytes < need)
@@ -616,7 +630,7 @@ I8L_API i8l_status int8_tree_attention(
   const i8l::TreeArgs a{{c, s, q, q_token_stride, q_head_stride, out, rows, G, (int)max_q,
                          (int)max_len, (int)window, scale, alibi, static_cast<float*>(workspace), 1, 0},
                         masks, words, positions, k, v, k_token_stride, k_head_stride,
-                        v_token_stride, v_head_stride};
+                        v_token_stride, v_head_stride, 0};
   return hip_status(fn, i8l::launch_tree_attention(a, static_cast<hipStream_t>(stream)));
 }
 

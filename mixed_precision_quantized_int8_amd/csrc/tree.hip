@@ -107,6 +107,14 @@ hipError_t launch_tree_accept(const TreeRows& r, const int64_t* tokens, const in
   return hipGetLastError();
 }
 
+size_t tree_partials(int B, int H, int G, int D, int max_q, int max_len, int window) {
+  const Plan p = plan(B, H, G, D, max_q, max_len, window);
+  if (const int n = tree_shares(p, B, H, G, max_q, max_len, window))
+    return kShareHead + 2 * (size_t)n * H * p.rows * (D + 2);
+  const size_t count = (size_t)B * H * G * max_q * p.n_split;
+  return p.n_split == 1 ? 0 : part_head(count) + count * D;
+}
+
 hipError_t launch_tree_attention(const TreeArgs& a, hipStream_t stream) {
   return launch_planned<true>(a, stream);
 }

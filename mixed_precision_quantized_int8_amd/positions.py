@@ -26,7 +26,7 @@ import torch
 from . import _binding
 from ._binding import check, lib
 from .serving import (KVCache, _dense, _half_type, _inference, _on, _one_each, _result, _scratch,
-                      _sequences, _stream, attention_workspace_bytes)
+                      _sequences, _stream)
 
 MAX_DRAFTS = 512   # of one sequence (I8L_MAX_DRAFTS)
 _byref = ctypes.byref
@@ -309,6 +309,11 @@ def tree_plan(parents, lengths, cu=None, max_q=None, positions=None, masks=None)
     return positions, masks
 
 
+def tree_workspace_bytes(cache, n, q_heads, max_q, max_len, window=0):
+    """Bytes of scratch that ``tree_attention`` uses for these sizes."""
+    return int(lib().i8l_tree_workspace_bytes(_byref(cache._struct), n, q_heads, max_q, max_len, window))
+
+
 def tree_attention(q, k, v, cache, page_table, lengths, masks, positions=None, cu=None, slots=None,
                    max_q=None, max_len=None, scale=None, window=0, alibi=None, out=None,
                    workspace=None):
@@ -322,7 +327,7 @@ def tree_attention(q, k, v, cache, page_table, lengths, masks, positions=None, c
     before the draft's) or ``alibi``.  A row with nothing to see gives 0.  ``max_q`` (None: 1
     without cu, else all rows, or what masks have bits for): at least the drafts of any one
     sequence; drafts past it are neither seen nor answered.  Everything else, the workspace
-    too (``attention_workspace_bytes``), as for ``cache_attention``.
+    too (``tree_workspace_bytes``), as for ``cache_attention``.
     """
     _inference(q, k, v, alibi)
     s = _sequences(cache, page_table, lengths, cu, slots)
@@ -341,7 +346,7 @@ def tree_attention(q, k, v, cache, page_table, lengths, masks, positions=None, c
         max_len = s.max_pages * cache.page_size
     out, op = _result(out, dt, (rows, heads, D), dev, "out")
     need = 0 if workspace is not None else \
-        attention_workspace_bytes(cache, s.n, heads, max_q, max_len, window)
+        tree_workspace_bytes(cache, s.n, heads, max_q, max_len, window)
     hold, ws, nb = _scratch(workspace, need, dev)
     with _on(dev):
         check(lib().int8_tree_attention(

@@ -176,7 +176,9 @@ def test_tree_refusals(i8l):
                 dict(alibi=P16 + 1), dict(out=None), dict(out=P8), dict(seqs=seqs_struct(max_pages=0))):
         assert attend(**bad) == INVALID, bad
         assert "int8_tree_attention: " in i8l.last_error()
-    need = L.i8l_attention_workspace_bytes(ref(cache_struct()), 2, 8, 1, 100000, 0)
+    need = L.i8l_tree_workspace_bytes(ref(cache_struct()), 2, 8, 1, 100000, 0)
+    assert need > 0 and L.i8l_tree_workspace_bytes(ref(cache_struct()), 2, 8, 1, 100, 0) == 0
+    assert L.i8l_tree_workspace_bytes(ref(cache_struct()), 2, 8, 513, 100000, 0) == 0
     assert attend(max_len=100000) == INVALID and "workspace is NULL" in i8l.last_error()
     assert attend(max_len=100000, ws=P16, n=need - 1) == WORKSPACE
     assert attend(rows=0) == OK and attend(seqs=seqs_struct(n=0)) == OK

@@ -536,7 +536,15 @@ TREES = [([100], [26], 8, 4, 128, 16, 0, False), ([37], [1], 2, 1, 64, 16, 0, Fa
          ([300, 17], [40, 130], 1, 8, 256, 16, 0, True), ([4000, 900], [16, 9], 4, 1, 128, 64, 0, True),
          ([9000], [12], 2, 2, 64, 128, 700, False), ([3000, 10, 2], [30, 70, 5], 2, 4, 128, 32, 100, True),
          ([640], [200], 1, 1, 112, 16, 64, False), ([500, 3], [90, 20], 2, 1, 16, 16, 9, False),
-         ([5000], [300], 1, 1, 128, 128, 0, False), ([257] * 5, [2, 0, 1, 33, 8], 2, 2, 64, 32, 3, True)]
+         ([5000], [300], 1, 1, 128, 128, 0, False), ([257] * 5, [2, 0, 1, 33, 8], 2, 2, 64, 32, 3, True),
+         ([6000, 5000], [150, 129], 1, 2, 128, 128, 0, True)]
+# keys shared out to workgroups by their number: several segments a workgroup, several
+# workgroups a tile, tiles without keys or drafts, two tiles of rows, any number of heads
+SHARED = [([2500, 130, 0, 700], [70, 33, 5, 64], 2, 4, 128, 16, 0, False),
+          ([3000, 64, 2100], [64, 0, 80], 5, 3, 64, 64, 0, True),
+          ([2200] + [100, 0, 257, 1] * 6, [40, 3, 20, 64, 0] * 5, 1, 8, 80, 32, 0, False),
+          ([9000, 5000], [150, 129], 1, 2, 128, 128, 0, True), ([2300, 2300], [33, 40], 7, 4, 96, 64, 0, False)]
+TREES += SHARED
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -557,6 +565,9 @@ def test_tree_attention(lib, case, dtype):
     masks = torch.cat([O.words(s, words) for s in seen]).cuda()
     slopes = torch.tensor([2.0 ** -(1 + 8 * (i + 1) / (H * G)) for i in range(H * G)]) if alibi else None
     out = torch.full((T + 3, H * G, D), 9.0, dtype=dt, device="cuda")
+    if case in SHARED:     # two places a workgroup for 256 rows' sums and outputs, 192 words before them
+        assert lib.tree_workspace_bytes(cache, len(lens), H * G, max(sizes), max(lens)) == \
+            4 * (192 + 2 * (256 // H) * H * 256 * (D + 2))
     got = lib.tree_attention(q, k, v, cache, table, ints(lens), masks, positions=ints(positions), cu=cu_of(sizes),
                              slots=slots, max_q=max(sizes), max_len=max(lens), scale=0.11, window=window,
                              alibi=None if slopes is None else slopes.cuda(), out=out[:T])
