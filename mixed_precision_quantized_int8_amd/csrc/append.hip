@@ -16,7 +16,7 @@ namespace i8l {
 template <bool BF, int LAYOUT, int BS, int NU>
 __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, const CacheRows& x,
                                             const HeadArgs& a, const uint16_t* k_w, int b, int h,
-                                            int task, float* row, uint32_t* red) {
+                                            int task, v4u* held, float* row, uint32_t* red) {
   constexpr int NT = 2 * NU;   // tokens a thread
   const int ps = c.ps, P = 1 << ps, D = c.D, t = threadIdx.x, lane = t & 63;
   const int lanes = lanes_of(D), j = t & (lanes - 1);
@@ -33,15 +33,21 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   const uint16_t* rows = x.x[0] + h * x.hs[0];
   const Runs at = runs_of<LAYOUT>(a.turn, j);
   const float inv = 1.0f / (float)D;
-  v4u w[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    w[r] = v4u{0, 0, 0, 0};
-    if (k_w && at.at[r] < D) w[r] = *reinterpret_cast<const v4u*>(k_w + at.at[r]);
-  }
-  // a token's 16 elements, normed and turned (every lane of the wave takes part)
+  // A token's 16 elements, normed and turned (every lane of the wave takes part).  Weights and
+  // frequencies come from the cache for each token: kept, their registers would cost waves.
   auto turned = [&](v4u (&p)[2], int pos) {
-    float y[16];
+    int zero = 0;
+    asm volatile("" : "+s"(zero));
+    float y[16], freq[Angles<LAYOUT>::N];
+    v4u w[2];
+#pragma unroll
+    for (int e = 0; e < Angles<LAYOUT>::N; ++e)
+      freq[e] = a.turn.pairs ? a.turn.freqs[zero + max(Angles<LAYOUT>::pair(a.turn, j, e), 0)] : 0.0f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      w[r] = v4u{0, 0, 0, 0};
+      if (k_w && at.at[r] < D) w[r] = *reinterpret_cast<const v4u*>(k_w + zero + at.at[r]);
+    }
     unpack<BF>(p, y);
     if (k_w) {
       const Rms m = rms_of<BF>(y, inv, lanes, a.eps);
@@ -52,43 +58,46 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
       for (int e = 0; e < 16; ++e) y[e] *= wf[e];
     }
     Angles<LAYOUT> angles;
-    angles.of(a.turn, j, false, [&](int i) { return angle(pos, a.turn.freqs[i], a.turn.factor); });
+    angles_at(angles, a.turn, j, pos, freq);
     turn<LAYOUT>(y, angles, a.turn, j, row, lane);
     pack<BF>(y, p);
   };
   if (g < full) {
     const int page = s.table[(size_t)b * s.max_pages + g];
     const bool page_ok = page >= 0 && page < c.n_pages;
-    v4u p[NT][2];
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
+    // A token at a time, the next one's elements on their way; what is turned waits in LDS
+    // for the page's maximum (a thread reads back what it wrote).
+    const auto load = [&](int u, v4u (&p)[2]) {
       const int tok = (t + u * BS) / lanes, pos = (g << ps) + tok;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        p[u][r] = v4u{0, 0, 0, 0};
+        p[r] = v4u{0, 0, 0, 0};
         if (tok < P && at.at[r] < D) {
           if (pos >= p0)
-            p[u][r] = *reinterpret_cast<const v4u*>(
-                rows + row_of<true>(x, sp.c0 + pos - p0) * x.ts[0] + at.at[r]);
+            p[r] = *reinterpret_cast<const v4u*>(rows + row_of<true>(x, sp.c0 + pos - p0) * x.ts[0] + at.at[r]);
           else if (slot_ok)
-            p[u][r] = *reinterpret_cast<const v4u*>(tail + tok * D + at.at[r]);
+            p[r] = *reinterpret_cast<const v4u*>(tail + tok * D + at.at[r]);
         }
       }
-    }
+    };
     // magnitudes of both types are in the order of their bits, infinities and NaNs last
     u16x2 mag = {0, 0};
-#pragma unroll
+    v4u next[2];
+    load(0, next);
+#pragma unroll 1
     for (int u = 0; u < NT; ++u) {
-      const int tok = (t + u * BS) / lanes, pos = (g << ps) + tok;
-      v4u q[2] = {p[u][0], p[u][1]};
+      v4u p[2] = {next[0], next[1]};
+      if (u + 1 < NT) load(u + 1, next);
+      const int pos = (g << ps) + (t + u * BS) / lanes;
+      v4u q[2] = {p[0], p[1]};
       turned(q, pos);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        if (pos >= p0) p[u][r] = q[r];   // (the tail's tokens are turned already)
-        if (tok < P && at.at[r] < D)
+        if (pos >= p0) p[r] = q[r];   // (the tail's tokens are turned already)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mag = __builtin_elementwise_max(mag, __builtin_bit_cast(u16x2, p[u][r][e] & 0x7fff7fffu));
+        for (int e = 0; e < 4; ++e)
+          mag = __builtin_elementwise_max(mag, __builtin_bit_cast(u16x2, p[r][e] & 0x7fff7fffu));
+        held[(u * 2 + r) * BS + t] = p[r];
       }
     }
     uint32_t bits = wave_max_u32(mag[0] > mag[1] ? mag[0] : mag[1]);
@@ -103,15 +112,16 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
     const float top = absmax < kLeastMax ? 0.0f : absmax;
     const float inv65 = (finite ? quant_scale(top) : 0.0f) * 65536.0f;
     int8_t* out = c.kc + ((size_t)(page_ok ? page : 0) * c.H + h) * P * D;
-#pragma unroll
+#pragma unroll 1
     for (int u = 0; u < NT; ++u) {
       const int tok = (t + u * BS) / lanes;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        const v4u p = held[(u * 2 + r) * BS + t];
         uint32_t z[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float f = to_f32<BF>((uint16_t)(p[u][r][e >> 1] >> (16 * (e & 1))));
+          const float f = to_f32<BF>((uint16_t)(p[e >> 1] >> (16 * (e & 1))));
           z[e] = code_bits(finite ? f : 0.0f, inv65);
         }
         uint2 k;
@@ -146,12 +156,16 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   }
 }
 
+// (80 registers, for six waves a SIMD: 24.8 k tokens, 32 heads on 8, 133 us, with 93
+// registers 137; keys kept in registers as values are, 126 of them, 148.  Halves through
+// LDS do not fit.)
 template <bool BF, int LAYOUT, int BS, int NU>
-__global__ __launch_bounds__(BS) void cache_append_kernel(Cache c, Sequences s, CacheRows x, HeadArgs a,
+__global__ __launch_bounds__(BS)
+__attribute__((amdgpu_waves_per_eu(LAYOUT == kTurnOdd ? 2 : 6))) void cache_append_kernel(Cache c, Sequences s, CacheRows x, HeadArgs a,
                                                           const uint16_t* k_w, uint32_t page_blocks,
                                                           int n_tok, int groups, int per_wg) {
-  // a page of values, or the angles of a workgroup's queries
-  __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 32];
+  // a page of keys in 16 bits, or of values in 8, or the angles of a workgroup's queries
+  __shared__ __attribute__((aligned(128))) uint8_t lds[BS * NU * 64];
   static_assert(sizeof(lds) >= 2048, "kTurnTokens * 64 angles; 128 come with twice the threads");
   __shared__ float s_turn[LAYOUT == kTurnOdd ? BS / 64 * kTurnRow : 1];
   __shared__ uint32_t red[BS / 64];
@@ -162,7 +176,7 @@ __global__ __launch_bounds__(BS) void cache_append_kernel(Cache c, Sequences s, 
     const uint32_t hk = blockIdx.x % (2 * c.H);
     const int task = blockIdx.x / (2 * c.H), h = hk >> 1;
     if (hk & 1) write_page<BF, true, BS, NU, true>(c, s, x, b, h, task, lds, red);
-    else append_keys<BF, LAYOUT, BS, NU>(c, s, x, a, k_w, b, h, task, row, red);
+    else append_keys<BF, LAYOUT, BS, NU>(c, s, x, a, k_w, b, h, task, reinterpret_cast<v4u*>(lds), row, red);
     return;
   }
   const uint32_t parts = (groups + per_wg - 1) / per_wg, q = blockIdx.x - page_blocks;
@@ -173,7 +187,7 @@ __global__ __launch_bounds__(BS) void cache_append_kernel(Cache c, Sequences s, 
   const int64_t i0 = (int64_t)(q / parts) * n_tok;
   if (i0 >= c1 - c0) return;
   const int g0 = q % parts * per_wg, pos0 = (int)(max(s.lengths[b], 0) - (c1 - c0) + i0);
-  turn_heads<BF, LAYOUT, BS / 64, false>(
+  turn_heads<BF, LAYOUT, BS / 64, 1, false>(
       a, c0 + i0, (int)min((int64_t)n_tok, c1 - c0 - i0), [&](int i) { return pos0 + i; }, g0,
       min(per_wg, groups - g0), lanes_of(a.D), reinterpret_cast<float2*>(lds), row);
 }
@@ -183,7 +197,7 @@ template <bool BF, int LAYOUT, int BS, int NU>
 void launch_sized(const Cache& c, const Sequences& s, const CacheRows& x, const HeadArgs& a,
                   const uint16_t* k_w, uint32_t page_blocks, int max_q, hipStream_t stream) {
   // the queries' workgroups, as launch_rows has them
-  const int per = 64 / lanes_of(c.D), groups = (a.side[0].n + per - 1) / per;
+  const int groups = head_groups(a, 0);
   const int n_tok = max_q >= 2048 ? kTurnTokens : 1;
   const int per_wg = n_tok == 1 && groups > BS / 64 && (int64_t)max_q * s.B * groups < 8192 ? BS / 64 : groups;
   const uint32_t q_blocks =

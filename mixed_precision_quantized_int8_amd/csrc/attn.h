@@ -511,6 +511,24 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
     auto draft_tile = [&](int t0) {
       const uint64_t word = draft_mask(a, sq, qi, t0 >> 6);
       uint32_t bits = live ? (uint32_t)(word >> (16 * grp)) & 0xffffu : 0u;   // this lane's 16 keys
+      // values of step st: drafts 16 g + 8 st + i of the tile are 8 g + i there, two neighbours
+      // of 8 dimensions a lane at a time; all on their way before they are needed
+      constexpr int NQ = 16 * (DP / 8) / 64;
+      v4u v[NQ][2];
+      auto load_values = [&](int st) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const int q = lane + 64 * n, i = 2 * (q & 15), d = (q >> 4) * 8;
+          const int key = t0 + 16 * (i >> 3) + 8 * st + (i & 7);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            v[n][u] = v4u{0, 0, 0, 0};
+            if (key + u < sq.n && d < D)
+              v[n][u] = *reinterpret_cast<const v4u*>(a.dv + (sq.c0 + key + u) * a.dv_ts + h * a.dv_hs + d);
+          }
+        }
+      };
+      load_values(0);
       v4f s[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -550,28 +568,23 @@ __global__ __launch_bounds__(kAdThreads, DP > 128 ? 1 : 2) void attn_decode_kern
       uint32_t odd = 0;
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        // drafts 16 g + 8 st + i of the tile are 8 g + i here; two neighbours a lane at a time
-        for (int q = lane; q < 16 * (DP / 8); q += 64) {
-          const int i = 2 * (q & 15), d = (q >> 4) * 8;
-          const int key = t0 + 16 * (i >> 3) + 8 * st + (i & 7);
-          v4u v[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            v[u] = v4u{0, 0, 0, 0};
-            if (key + u < sq.n && d < D)
-              v[u] = *reinterpret_cast<const v4u*>(a.dv + (sq.c0 + key + u) * a.dv_ts + h * a.dv_hs + d);
+        for (int n = 0; n < NQ; ++n) {
+          const int q = lane + 64 * n, i = 2 * (q & 15), d = (q >> 4) * 8;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t bad = odd_halves<BF>(v[u][e]);
+              const uint32_t bad = odd_halves<BF>(v[n][u][e]);
               odd |= bad;
-              v[u][e] = clear_halves(v[u][e], bad);
+              v[n][u][e] = clear_halves(v[n][u][e], bad);
             }
-          }
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<uint32_t*>(turned + (d + e) * 64 + 2 * i) =
-                __builtin_amdgcn_perm(v[1][e >> 1], v[0][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
+                __builtin_amdgcn_perm(v[n][1][e >> 1], v[n][0][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
         }
+        if (st == 0) load_values(1);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         const v4u p = weights(s, st);

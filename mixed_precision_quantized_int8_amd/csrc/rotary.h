@@ -40,46 +40,82 @@ __device__ __forceinline__ Runs runs_of(const Turn& r, int j) {
   return Runs{{16 * j, 16 * j + 8}};
 }
 
-// cos and sin (times the factor) of one pair's angle.  position * freq is formed in 64
-// bits, since at position 10^6 a 32-bit product is off by 0.06 radians, and reduced to
-// half a turn there; the hardware's sine and cosine of turns are then within 1.3e-7
-// (measured over that range), and a third of the time of a series.
-__device__ __forceinline__ float2 angle(int pos, float freq, float f) {
+// cos and sin (times the factor) of one pair's angle, position * freq reduced to half a
+// turn: a 32-bit product alone is off by 0.06 radians at position 10^6.  Up to 2^20 turns
+// the product is formed in two parts, each exact or below 2^-25 of a turn (the part past
+// the first 24 bits of freq / 2 pi, what the product's rounding left); past that in 64
+// bits, which takes three times as long.  The hardware's sine and cosine of turns are
+// within 1.3e-7 over half a turn (measured).
+__device__ __forceinline__ float near_turns(int pos, float freq, bool* far) {
 #pragma clang fp contract(off)   // (the same bits wherever it is inlined)
-  double t = (double)pos * (double)freq * 0.15915494309189533577;   // turns
-  t -= __builtin_rint(t);
-  const float u = (float)t;                          // -1/2 .. 1/2
+  constexpr float kTurn = 0.15915494f;                              // 1 / 2 pi
+  constexpr float kRest = (float)(0.15915494309189533577 - (double)kTurn);
+  const float p = (float)pos, h = freq * kTurn, t = p * h;
+  const float l = __builtin_fmaf(freq, kRest, __builtin_fmaf(freq, kTurn, -h));
+  *far = !(__builtin_fabsf(t) < 0x1p20f && __builtin_fabsf(p) < 0x1p24f);
+  return (t - __builtin_rintf(t)) + __builtin_fmaf(p, l, __builtin_fmaf(p, h, -t));
+}
+__device__ __forceinline__ float far_turns(int pos, float freq) {
+#pragma clang fp contract(off)
+  const double t = (double)pos * (double)freq * 0.15915494309189533577;
+  return (float)(t - __builtin_rint(t));
+}
+__device__ __forceinline__ float2 turned_by(float u, float f) {
   return make_float2(f * __builtin_amdgcn_cosf(u), f * __builtin_amdgcn_sinf(u));
 }
+__device__ __forceinline__ float2 angle(int pos, float freq, float f) {
+  bool far;
+  float u = near_turns(pos, freq, &far);
+  if (far) u = far_turns(pos, freq);
+  return turned_by(u, f);
+}
 
-// The 8 (kTurnOdd: 16) angles of a thread, each from `get(i)`, pair i's cos and sin; an
-// element past the pairs has angle 0 and factor 1.  `back`: the other way.
+// The 8 (kTurnOdd: 16) angles of a thread, from get(i, e), pair i's cos and sin for place
+// e; a place past the pairs has angle 0 and factor 1 (its i is 0: no branch, so that what
+// get loads is on its way together).  `back`: the other way.
 template <int LAYOUT>
 struct Angles {
   static constexpr int N = LAYOUT == kTurnOdd ? 16 : 8;
   float c[N], s[N];
+  // pair of place e, -1: none
+  static __device__ __forceinline__ int pair(const Turn& r, int j, int e) {
+    const int h = r.pairs;
+    if (LAYOUT == kTurnHalves) return 8 * j < h ? 8 * j + e : -1;
+    if (LAYOUT == kTurnPairs) return 8 * j + e < h ? 8 * j + e : -1;
+    const int d = 16 * j + e;
+    return d < h ? d : d < 2 * h ? d - h : -1;
+  }
   template <class Get>
   __device__ __forceinline__ void of(const Turn& r, int j, bool back, Get get) {
-    const int h = r.pairs;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      int i = 8 * j + e;
-      bool on = i < h;
-      bool second = false;
-      if (LAYOUT == kTurnOdd) {
-        const int d = 16 * j + e;
-        on = d < 2 * h;
-        second = d >= h;
-        i = second ? d - h : d;
-      }
+      const int i = pair(r, j, e);
       float2 a = make_float2(1.0f, 0.0f);
-      if (on) a = get(i);
-      c[e] = a.x;
-      s[e] = back ? -a.y : a.y;
-      if (LAYOUT == kTurnOdd && !second) s[e] = -s[e];   // y_a = a c + b (-s), y_b = b c + a s
+      if (r.pairs) a = get(max(i, 0), e);   // uniform
+      c[e] = i < 0 ? 1.0f : a.x;
+      s[e] = i < 0 ? 0.0f : back ? -a.y : a.y;
+      if (LAYOUT == kTurnOdd && 16 * j + e < r.pairs) s[e] = -s[e];   // y_a = a c + b (-s), y_b = b c + a s
     }
   }
 };
+
+// The angles of a thread at one position, freq[e] that of place e.
+template <int LAYOUT>
+__device__ __forceinline__ void angles_at(Angles<LAYOUT>& a, const Turn& r, int j, int pos,
+                                          const float (&freq)[Angles<LAYOUT>::N]) {
+  constexpr int N = Angles<LAYOUT>::N;
+  float u[N];
+  bool far[N], some = false;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    u[e] = near_turns(pos, freq[e], &far[e]);
+    some |= far[e];
+  }
+  if (__any(some))
+#pragma unroll
+    for (int e = 0; e < N; ++e) u[e] = far[e] ? far_turns(pos, freq[e]) : u[e];
+  a.of(r, j, false, [&](int, int e) { return turned_by(u[e], r.factor); });
+}
 
 // x turned in place: x[8 r + e] is element e of run r.  kTurnOdd: `row` is this wave's
 // kTurnRow floats of LDS.
@@ -190,42 +226,47 @@ __device__ __forceinline__ void over_rms(float (&x)[16], const Rms& m) {
 }
 
 // The heads of some tokens, by a workgroup of NW waves: tok0 .. tok0 + n_tok - 1 at
-// positions pos(0) .. pos(n_tok - 1), the groups of 64 / lanes_of(D) heads from g0 on, ng
-// of them.  The angles are formed once, into s_cs (n_tok * pairs), and a wave takes a token's
-// group at a time, with the next one's elements on their way.  BACK: the gradient without
-// a norm, dy turned the other way.
+// positions pos(0) .. pos(n_tok - 1), the groups of heads from g0 on, ng of them: a group
+// is 64 / lanes_of(D) heads of one side, the first side's groups first (SIDES 1: there is
+// no other).  The angles are formed once, into s_cs (n_tok * pairs), and a wave takes a
+// token's group at a time, with the next one's elements on their way.  BACK: the gradient
+// without a norm, dy turned the other way.
 constexpr int kTurnTokens = 4;   // at most n_tok
 constexpr int kMaxPairs = 128;
-template <bool BF, int LAYOUT, int NW, bool BACK, class Pos>
+__host__ __device__ inline int head_groups(const HeadArgs& a, int k) {
+  const int per = 64 / lanes_of(a.D);
+  return (a.side[k].n + per - 1) / per;
+}
+template <bool BF, int LAYOUT, int NW, int SIDES, bool BACK, class Pos>
 __device__ __forceinline__ void turn_heads(const HeadArgs& a, int64_t tok0, int n_tok, Pos pos, int g0,
                                            int ng, int lanes, float2* s_cs, float* row) {
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int j = lane & (lanes - 1), sub = lane / lanes, per = 64 / lanes;
-  const int n0 = a.side[0].n, all = n0 + a.side[1].n, D = a.D, pairs = a.turn.pairs;
+  const int D = a.D, pairs = a.turn.pairs, groups0 = SIDES > 1 ? head_groups(a, 0) : 0;
   const Runs at = runs_of<LAYOUT>(a.turn, j);
   const float inv = 1.0f / (float)D;
-  const bool norms = !BACK && (a.side[0].w || a.side[1].w);
-  v4u w[2][2];   // this lane's weights of both sides
+  v4u w[SIDES][2];   // this lane's weights
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < SIDES; ++k)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       w[k][r] = v4u{0, 0, 0, 0};
       if (!BACK && a.side[k].w && at.at[r] < D)
         w[k][r] = *reinterpret_cast<const v4u*>(a.side[k].w + at.at[r]);
     }
+  // (side and first head of a group are the same for the wave: they stay in scalar registers)
+  auto side_of = [&](int g) { return SIDES > 1 && g0 + g >= groups0 ? 1 : 0; };
+  auto head_of = [&](int g) { return (g0 + g - (side_of(g) ? groups0 : 0)) * per + sub; };
   auto load = [&](int i, int g, v4u (&p)[2]) {
-    const int hh = (g0 + g) * per + sub;
-    const bool k = hh >= n0;
-    const auto& sd = a.side[k];
-    const int64_t h = hh - (k ? n0 : 0);
+    const auto& sd = a.side[side_of(g)];
+    const int h = head_of(g);
     const uint16_t* x = BACK ? sd.dy + (tok0 + i) * sd.dy_ts + h * sd.dy_hs
                              : sd.x + (tok0 + i) * sd.x_ts + h * sd.x_hs;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       p[r] = v4u{0, 0, 0, 0};
-      if (hh < all && at.at[r] < D) p[r] = *reinterpret_cast<const v4u*>(x + at.at[r]);
+      if (h < sd.n && at.at[r] < D) p[r] = *reinterpret_cast<const v4u*>(x + at.at[r]);
     }
   };
   // this wave's token and group: the wave'th of them in order, then every NW'th
@@ -245,30 +286,28 @@ __device__ __forceinline__ void turn_heads(const HeadArgs& a, int64_t tok0, int 
     int i1 = i, g1 = g + NW;
     settle(i1, g1);
     if (i1 < n_tok) load(i1, g1, next);
-    const int hh = (g0 + g) * per + sub;
-    const bool k = hh >= n0;
+    const int k = side_of(g);
     const auto& sd = a.side[k];
     Angles<LAYOUT> angles;
-    angles.of(a.turn, j, BACK, [&](int e) { return s_cs[i * pairs + e]; });
+    angles.of(a.turn, j, BACK, [&](int q, int) { return s_cs[i * pairs + q]; });
     float x[16];
     unpack<BF>(p, x);
-    if (norms) {
+    if (!BACK && sd.w) {   // uniform
       const Rms m = rms_of<BF>(x, inv, lanes, a.eps);
-      if (sd.w) {
-        float wf[16];
-        const v4u wk[2] = {k ? w[1][0] : w[0][0], k ? w[1][1] : w[0][1]};
-        unpack<BF>(wk, wf);
-        over_rms(x, m);
+      float wf[16];
+      const v4u wk[2] = {w[SIDES - 1][0], w[SIDES - 1][1]};
+      unpack<BF>(SIDES > 1 && k == 0 ? w[0] : wk, wf);
+      over_rms(x, m);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= wf[e];
-      }
+      for (int e = 0; e < 16; ++e) x[e] *= wf[e];
     }
     turn<LAYOUT>(x, angles, a.turn, j, row, lane);
     pack<BF>(x, p);
-    uint16_t* y = sd.y + (tok0 + i) * sd.y_ts + (int64_t)(hh - (k ? n0 : 0)) * sd.y_hs;
+    const int h = head_of(g);
+    uint16_t* y = sd.y + (tok0 + i) * sd.y_ts + h * sd.y_hs;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      if (hh < all && at.at[r] < D) *reinterpret_cast<v4u*>(y + at.at[r]) = p[r];
+      if (h < sd.n && at.at[r] < D) *reinterpret_cast<v4u*>(y + at.at[r]) = p[r];
       p[r] = next[r];
     }
     i = i1;

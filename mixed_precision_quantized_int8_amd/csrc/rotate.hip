@@ -12,7 +12,7 @@ namespace i8l {
 
 constexpr int kRotThreads = 256, kRotWaves = kRotThreads / 64;
 
-template <bool BF, int LAYOUT, bool BACK>
+template <bool BF, int LAYOUT, int SIDES, bool BACK>
 __global__ __launch_bounds__(kRotThreads) void rotate_heads_kernel(HeadArgs a, int lanes, int n_tok,
                                                                    int groups, int per_wg) {
   __shared__ float2 s_cs[kTurnTokens * kMaxPairs];
@@ -20,7 +20,7 @@ __global__ __launch_bounds__(kRotThreads) void rotate_heads_kernel(HeadArgs a, i
   const int64_t tok0 = (int64_t)blockIdx.x * n_tok;
   const int g0 = blockIdx.y * per_wg;
   const int32_t* pos = a.positions + tok0;
-  turn_heads<BF, LAYOUT, kRotWaves, BACK>(
+  turn_heads<BF, LAYOUT, kRotWaves, SIDES, BACK>(
       a, tok0, (int)min((int64_t)n_tok, a.rows - tok0), [&](int i) { return pos[i]; }, g0,
       min(per_wg, groups - g0), lanes, s_cs,
       s_turn + (LAYOUT == kTurnOdd ? (threadIdx.x >> 6) * kTurnRow : 0));
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kRotThreads) void rotate_grad_kernel(HeadArgs a, in
       if (i1 < n) load(i1, g1, p1, q1);
       const int64_t hh = g * per + sub;
       Angles<LAYOUT> angles;
-      angles.of(a.turn, j, true, [&](int e) { return s_cs[i * pairs + e]; });
+      angles.of(a.turn, j, true, [&](int q, int) { return s_cs[i * pairs + q]; });
       float y[16];
       unpack<BF>(p, y);
       turn<LAYOUT>(y, angles, a.turn, j, row, lane);
@@ -166,13 +166,16 @@ namespace {
 // once, one or two a thread.  Otherwise one, and a group of heads a wave.
 template <bool BF, int LAYOUT, bool BACK>
 void launch_rows(const HeadArgs& a, hipStream_t stream) {
-  const int lanes = lanes_of(a.D), per = 64 / lanes;
-  const int groups = (a.side[0].n + a.side[1].n + per - 1) / per;
+  const int lanes = lanes_of(a.D), groups = head_groups(a, 0) + head_groups(a, 1);
   const int n_tok = a.rows >= 2048 ? kTurnTokens : 1;
   const int per_wg = n_tok == 1 && groups > kRotWaves && (int64_t)a.rows * groups < 8192 ? kRotWaves : groups;
-  hipLaunchKernelGGL((rotate_heads_kernel<BF, LAYOUT, BACK>),
-                     dim3((a.rows + n_tok - 1) / n_tok, (groups + per_wg - 1) / per_wg),
-                     dim3(kRotThreads), 0, stream, a, lanes, n_tok, groups, per_wg);
+  const dim3 grid((a.rows + n_tok - 1) / n_tok, (groups + per_wg - 1) / per_wg);
+  if (a.side[1].n)
+    hipLaunchKernelGGL((rotate_heads_kernel<BF, LAYOUT, 2, BACK>), grid, dim3(kRotThreads), 0, stream, a,
+                       lanes, n_tok, groups, per_wg);
+  else
+    hipLaunchKernelGGL((rotate_heads_kernel<BF, LAYOUT, 1, BACK>), grid, dim3(kRotThreads), 0, stream, a,
+                       lanes, n_tok, groups, per_wg);
 }
 
 int grad_tokens(int rows) { return rows >= 4096 ? kTurnTokens : 1; }

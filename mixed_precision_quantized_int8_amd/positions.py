@@ -24,12 +24,24 @@ import math
 import torch
 
 from . import _binding
-from ._binding import check, lib
-from .serving import (KVCache, _dense, _half_type, _inference, _on, _one_each, _result, _scratch,
-                      _sequences, _stream)
+from ._binding import HeadsGradStruct, HeadsStruct, RotaryStruct, check, lib
+from .serving import (_dense, _half_type, _inference, _one_each, _result, _scratch, _sequences,
+                      _stream)
 
 MAX_DRAFTS = 512   # of one sequence (I8L_MAX_DRAFTS)
 _byref = ctypes.byref
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(device, f, *args):
+    """f on the device's current stream, the device the current one for the call."""
+    if device.index == _current():
+        status = f(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, _stream(device))
+    if status:
+        check(status)
 
 
 class Rotary:
@@ -45,12 +57,15 @@ class Rotary:
 
     def __init__(self, freqs, interleaved=False, factor=1.0):
         n = freqs.numel() if isinstance(freqs, torch.Tensor) else 0
-        struct = _binding.RotaryStruct(_dense(freqs, torch.float32, (n,), None, "freqs"), n,
-                                       1 if interleaved else 0, float(factor))
+        at = _dense(freqs, torch.float32, (n,), None, "freqs")
+        factor, interleaved = float(factor), bool(interleaved)
         if not math.isfinite(factor):
             raise ValueError(f"factor must be finite, got {factor}")
-        for put, x in zip(_ROTARY_FIELDS, (freqs, bool(interleaved), float(factor), freqs.device, struct)):
-            put(self, x)
+        _put_freqs(self, freqs)
+        _put_interleaved(self, interleaved)
+        _put_factor(self, factor)
+        _put_device(self, freqs.device)
+        _put_struct(self, RotaryStruct(at, n, interleaved, factor))
 
     def __setattr__(self, name, x):
         raise AttributeError(f"{name}: a Rotary does not change; make a new one")
@@ -60,7 +75,8 @@ class Rotary:
 
 
 # what the constructor writes an unchanging object's attributes with
-_ROTARY_FIELDS = [Rotary.__dict__[name].__set__ for name in Rotary.__slots__]
+_put_freqs, _put_interleaved, _put_factor, _put_device, _put_struct = (
+    Rotary.__dict__[name].__set__ for name in Rotary.__slots__)
 
 
 def rotary(dim, base=10000.0, interleaved=False, scaling=None, scale=1.0, original=None, low=1.0,
@@ -111,22 +127,24 @@ def _turn(rot, device):
     return _byref(rot._struct)
 
 
-def _heads(t, dtype, device, shape, name):
-    """(pointer, token stride, head stride) of a [rows][heads][head_dim] tensor; shape: its
-    rows, heads and head_dim (None: any)."""
+def _heads(t, dtype, device, rows, heads, D, name):
+    """(pointer, token stride, head stride) of a [rows][heads][D] tensor (None: any number);
+    what is right is settled first, what is wrong said after, as in serving._dense."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.dim() == 3:
+        n, h, d = t.shape
+        if (rows is None or n == rows) and (heads is None or h == heads) and d == D:
+            st, sh, sd = t.stride()
+            if sd == 1 or D == 1:
+                return t.data_ptr(), st, sh
+            raise ValueError(f"{name} must be contiguous in its last dimension")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.device != device:
         raise ValueError(f"{name} must be on {device} (got {t.device})")
-    if t.dim() != 3 or any(want is not None and got != want for got, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} must be [{']['.join('any' if s is None else str(s) for s in shape)}], "
-                         f"got {list(t.shape)}")
-    st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t.data_ptr(), st, sh
+    shape = "][".join("any" if s is None else str(s) for s in (rows, heads, D))
+    raise ValueError(f"{name} must be [{shape}], got {list(t.shape)}")
 
 
 def _weight(w, dtype, D, device, name):
@@ -135,12 +153,14 @@ def _weight(w, dtype, D, device, name):
 
 def _side(x, weight, out, dtype, device, rows, D, name):
     """(struct, output) of one tensor of heads."""
-    p, ts, hs = _heads(x, dtype, device, (rows, None, D), name)
+    p, ts, hs = _heads(x, dtype, device, rows, None, D, name)
     H = x.shape[1]
     if out is None:
         out = torch.empty((rows, H, D), dtype=dtype, device=device)
-    y, yts, yhs = _heads(out, dtype, device, (rows, H, D), name + "_out")
-    return _binding.HeadsStruct(p, ts, hs, y, yts, yhs,
+        y, yts, yhs = out.data_ptr(), H * D, D
+    else:
+        y, yts, yhs = _heads(out, dtype, device, rows, H, D, name + "_out")
+    return HeadsStruct(p, ts, hs, y, yts, yhs,
                                 _weight(weight, dtype, D, device, name + "_weight"), H), out
 
 
@@ -165,28 +185,28 @@ def rotate_heads(q, positions, rotary=None, k=None, q_weight=None, k_weight=None
         ks, k_out = _side(k, k_weight, k_out, dt, dev, rows, D, "k")
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight or k_out without k")
-    with _on(dev):
-        check(lib().int8_rotate_heads(_byref(qs), None if ks is None else _byref(ks), D, rows,
-                                      _dense(positions, torch.int32, (rows,), dev, "positions"),
-                                      _turn(rotary, dev), float(eps), code, _stream(dev)))
+    _call(dev, lib().int8_rotate_heads, _byref(qs), None if ks is None else _byref(ks), D, rows,
+          _dense(positions, torch.int32, (rows,), dev, "positions"), _turn(rotary, dev), float(eps), code)
     return q_out if k is None else (q_out, k_out)
 
 
 def _grad_side(dy, x, weight, out, dtype, device, rows, D, name):
     """(struct, dx, dweight) of one tensor of heads."""
-    p, ts, hs = _heads(dy, dtype, device, (rows, None, D), "d" + name)
+    p, ts, hs = _heads(dy, dtype, device, rows, None, D, "d" + name)
     H = dy.shape[1]
     w = _weight(weight, dtype, D, device, name + "_weight")
     xp, xts, xhs, dw = None, 0, 0, None
     if weight is not None:
         if x is None:
             raise ValueError(f"{name} (the forward pass's input) is needed with {name}_weight")
-        xp, xts, xhs = _heads(x, dtype, device, (rows, H, D), name)
+        xp, xts, xhs = _heads(x, dtype, device, rows, H, D, name)
         dw = torch.empty((D,), dtype=dtype, device=device)
     if out is None:
         out = torch.empty((rows, H, D), dtype=dtype, device=device)
-    y, yts, yhs = _heads(out, dtype, device, (rows, H, D), f"d{name}_out")
-    return _binding.HeadsGradStruct(p, ts, hs, xp, xts, xhs, y, yts, yhs, w,
+        y, yts, yhs = out.data_ptr(), H * D, D
+    else:
+        y, yts, yhs = _heads(out, dtype, device, rows, H, D, f"d{name}_out")
+    return HeadsGradStruct(p, ts, hs, xp, xts, xhs, y, yts, yhs, w,
                                     None if dw is None else dw.data_ptr(), H), out, dw
 
 
@@ -213,11 +233,9 @@ def rotate_heads_backward(dq, positions, rotary=None, q=None, dk=None, k=None, q
     if workspace is None and (dqw is not None or dkw is not None):
         need = rotate_heads_workspace_bytes(rows, D)
     hold, ws, nb = _scratch(workspace, need, dev)
-    with _on(dev):
-        check(lib().int8_rotate_heads_backward(
-            _byref(qs), None if ks is None else _byref(ks), D, rows,
-            _dense(positions, torch.int32, (rows,), dev, "positions"), _turn(rotary, dev), float(eps),
-            code, ws, nb, _stream(dev)))
+    _call(dev, lib().int8_rotate_heads_backward, _byref(qs), None if ks is None else _byref(ks), D, rows,
+          _dense(positions, torch.int32, (rows,), dev, "positions"), _turn(rotary, dev), float(eps), code,
+          ws, nb)
     return dq_out, dk_out, dqw, dkw
 
 
@@ -242,8 +260,8 @@ def cache_append(cache, k, v, page_table, lengths, q=None, rotary=None, q_weight
     _inference(q, k, v, q_weight, k_weight)
     s = _sequences(cache, page_table, lengths, cu, slots)
     D, dt, dev = cache.head_dim, cache.dtype, cache.device
-    kp, kt, kh = _heads(k, dt, dev, (None, cache.heads, D), "k")
-    vp, vt, vh = _heads(v, dt, dev, (k.shape[0], cache.heads, D), "v")
+    kp, kt, kh = _heads(k, dt, dev, None, cache.heads, D, "k")
+    vp, vt, vh = _heads(v, dt, dev, k.shape[0], cache.heads, D, "v")
     kv_rows = k.shape[0]
     ip, rows = None, kv_rows
     if index is not None:
@@ -263,12 +281,10 @@ def cache_append(cache, k, v, page_table, lengths, q=None, rotary=None, q_weight
         raise ValueError("q_weight or q_out without q")
     if max_new is None:
         max_new = 1 if cu is None else rows
-    with _on(dev):
-        check(lib().int8_cache_append(
-            _byref(cache._struct), _byref(s),
-            None if counts is None else _dense(counts, torch.int32, (s.n,), dev, "counts"), ip, kp, kt, kh,
-            vp, vt, vh, kv_rows, rows, int(max_new), None if qs is None else _byref(qs),
-            _weight(k_weight, dt, D, dev, "k_weight"), _turn(rotary, dev), float(eps), _stream(dev)))
+    _call(dev, lib().int8_cache_append, _byref(cache._struct), _byref(s),
+          None if counts is None else _dense(counts, torch.int32, (s.n,), dev, "counts"), ip, kp, kt, kh,
+          vp, vt, vh, kv_rows, rows, int(max_new), None if qs is None else _byref(qs),
+          _weight(k_weight, dt, D, dev, "k_weight"), _turn(rotary, dev), float(eps))
     return q_out
 
 
@@ -304,8 +320,7 @@ def tree_plan(parents, lengths, cu=None, max_q=None, positions=None, masks=None)
     words = -(-max_q // 64) if masks is None else masks.shape[1]
     positions, op = _result(positions, torch.int32, (rows,), dev, "positions")
     masks, mp = _result(masks, torch.int64, (rows, words), dev, "masks")
-    with _on(dev):
-        check(lib().int8_tree_plan(pp, lp, cp, n, rows, max_q, op, mp, words, _stream(dev)))
+    _call(dev, lib().int8_tree_plan, pp, lp, cp, n, rows, max_q, op, mp, words)
     return positions, masks
 
 
@@ -332,10 +347,10 @@ def tree_attention(q, k, v, cache, page_table, lengths, masks, positions=None, c
     _inference(q, k, v, alibi)
     s = _sequences(cache, page_table, lengths, cu, slots)
     D, dt, dev = cache.head_dim, cache.dtype, cache.device
-    qp, qt, qh = _heads(q, dt, dev, (None, None, D), "q")
+    qp, qt, qh = _heads(q, dt, dev, None, None, D, "q")
     rows, heads, _ = q.shape
-    kp, kt, kh = _heads(k, dt, dev, (rows, cache.heads, D), "k")
-    vp, vt, vh = _heads(v, dt, dev, (rows, cache.heads, D), "v")
+    kp, kt, kh = _heads(k, dt, dev, rows, cache.heads, D, "k")
+    vp, vt, vh = _heads(v, dt, dev, rows, cache.heads, D, "v")
     _one_each(q, s.n, cu, "q")
     if not isinstance(masks, torch.Tensor) or masks.dim() != 2:
         raise ValueError("masks must be an int64 tensor [rows][words]")
@@ -348,14 +363,12 @@ def tree_attention(q, k, v, cache, page_table, lengths, masks, positions=None, c
     need = 0 if workspace is not None else \
         tree_workspace_bytes(cache, s.n, heads, max_q, max_len, window)
     hold, ws, nb = _scratch(workspace, need, dev)
-    with _on(dev):
-        check(lib().int8_tree_attention(
-            _byref(cache._struct), _byref(s), qp, qt, qh, heads, kp, kt, kh, vp, vt, vh, rows,
-            int(max_q), int(max_len), _dense(masks, torch.int64, (rows, words), dev, "masks"), words,
-            None if positions is None else _dense(positions, torch.int32, (rows,), dev, "positions"),
-            float(D ** -0.5 if scale is None else scale), int(window),
-            None if alibi is None else _dense(alibi, torch.float32, (heads,), dev, "alibi"), op, ws, nb,
-            _stream(dev)))
+    _call(dev, lib().int8_tree_attention, _byref(cache._struct), _byref(s), qp, qt, qh, heads, kp, kt, kh,
+          vp, vt, vh, rows, int(max_q), int(max_len),
+          _dense(masks, torch.int64, (rows, words), dev, "masks"), words,
+          None if positions is None else _dense(positions, torch.int32, (rows,), dev, "positions"),
+          float(D ** -0.5 if scale is None else scale), int(window),
+          None if alibi is None else _dense(alibi, torch.float32, (heads,), dev, "alibi"), op, ws, nb)
     return out
 
 
@@ -375,13 +388,11 @@ def tree_accept(parents, tokens, choices, lengths, cu=None, first=None, max_q=No
     rows, n, max_q, dev, (pp, lp, cp) = _tree(parents, lengths, cu, max_q)
     # (one allocation: path, counts, lengths)
     ints = torch.empty((rows + 2 * n,), dtype=torch.int32, device=dev)
-    path, counts, longer = ints[:rows], ints[rows:rows + n], ints[rows + n:]
+    path, counts, longer = ints.split([rows, n, n])
     after = torch.empty((n,), dtype=torch.int64, device=dev)
     at = ints.data_ptr()
-    with _on(dev):
-        check(lib().int8_tree_accept(
-            pp, _dense(tokens, torch.int64, (rows,), dev, "tokens"),
-            _dense(choices, torch.int64, (rows,), dev, "choices"),
-            None if first is None else _dense(first, torch.int64, (n,), dev, "first"), lp, cp, n, rows,
-            max_q, at, at + 4 * rows, at + 4 * (rows + n), after.data_ptr(), _stream(dev)))
+    _call(dev, lib().int8_tree_accept, pp, _dense(tokens, torch.int64, (rows,), dev, "tokens"),
+          _dense(choices, torch.int64, (rows,), dev, "choices"),
+          None if first is None else _dense(first, torch.int64, (n,), dev, "first"), lp, cp, n, rows, max_q,
+          at, at + 4 * rows, at + 4 * (rows + n), after.data_ptr())
     return path, counts, longer, after
