@@ -447,7 +447,8 @@ typedef struct {
 } i8l_rotary;
 
 /* Heads to norm and turn.  Element (t, h, d) of x (of y) at t * token_stride +
- * h * head_stride + d: strides in elements, multiples of 8; pointers 16-byte aligned. */
+ * h * head_stride + d: strides in elements, multiples of 8; pointers 16-byte aligned; y's
+ * heads do not overlap one another. */
 typedef struct {
   const uint16_t *x;
   int64_t x_token_stride, x_head_stride;
@@ -475,7 +476,7 @@ typedef struct {
   int64_t dy_token_stride, dy_head_stride;
   const uint16_t *x;       /* the forward pass's input; unused (may be NULL) without weight */
   int64_t x_token_stride, x_head_stride;
-  uint16_t *dx;            /* out; may be dy or x, with its strides */
+  uint16_t *dx;            /* out; may be dy or x, with its strides; heads do not overlap */
   int64_t dx_token_stride, dx_head_stride;
   const uint16_t *weight;  /* as in the forward pass */
   uint16_t *dweight;       /* [head_dim] out, with weight; 2-byte aligned */
@@ -504,7 +505,8 @@ i8l_status int8_rotate_heads_backward(const i8l_heads_grad *q, const i8l_heads_g
  *   max_new   at least the rows of any one sequence
  *   q         NULL: no queries; q->y's rows outside the sequences are not written
  *   k_weight  [head_dim] or NULL;  rotary NULL: nothing turns
- * Everything else as for int8_cache_write. */
+ * Everything else as for int8_cache_write, but that rows for sequences without a page table
+ * (max_pages 0) are refused. */
 i8l_status int8_cache_append(const i8l_kv_cache *cache, const i8l_sequences *seqs,
                              const int32_t *counts, const int32_t *index, const uint16_t *k,
                              int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v,

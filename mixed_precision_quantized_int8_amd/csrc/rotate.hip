@@ -178,6 +178,11 @@ void launch_rows(const HeadArgs& a, hipStream_t stream) {
                        lanes, n_tok, groups, per_wg);
 }
 
+template <bool BF, int LAYOUT>
+void launch_forward(const HeadArgs& a, hipStream_t stream) {
+  launch_rows<BF, LAYOUT, false>(a, stream);
+}
+
 int grad_tokens(int rows) { return rows >= 4096 ? kTurnTokens : 1; }
 int grad_blocks(int rows) {
   const int n = grad_tokens(rows), blocks = (int)(((int64_t)rows + n - 1) / n);
@@ -198,22 +203,22 @@ void launch_grad(const HeadArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-#define I8L_TURN(F, ...)                                                       \
-  do {                                                                         \
-    const TurnLayout layout = turn_layout(a.turn);                             \
-    if (a.bf16) {                                                              \
-      if (layout == kTurnHalves) F<true, kTurnHalves __VA_ARGS__>(a, stream);  \
-      else if (layout == kTurnPairs) F<true, kTurnPairs __VA_ARGS__>(a, stream); \
-      else F<true, kTurnOdd __VA_ARGS__>(a, stream);                           \
-    } else {                                                                   \
-      if (layout == kTurnHalves) F<false, kTurnHalves __VA_ARGS__>(a, stream); \
-      else if (layout == kTurnPairs) F<false, kTurnPairs __VA_ARGS__>(a, stream); \
-      else F<false, kTurnOdd __VA_ARGS__>(a, stream);                          \
-    }                                                                          \
+#define I8L_TURN(F)                                                     \
+  do {                                                                  \
+    const TurnLayout layout = turn_layout(a.turn);                      \
+    if (a.bf16) {                                                       \
+      if (layout == kTurnHalves) F<true, kTurnHalves>(a, stream);       \
+      else if (layout == kTurnPairs) F<true, kTurnPairs>(a, stream);    \
+      else F<true, kTurnOdd>(a, stream);                                \
+    } else {                                                            \
+      if (layout == kTurnHalves) F<false, kTurnHalves>(a, stream);      \
+      else if (layout == kTurnPairs) F<false, kTurnPairs>(a, stream);   \
+      else F<false, kTurnOdd>(a, stream);                               \
+    }                                                                   \
   } while (0)
 
 hipError_t launch_rotate_heads(const HeadArgs& a, hipStream_t stream) {
-  I8L_TURN(launch_rows, , false);
+  I8L_TURN(launch_forward);
   return hipGetLastError();
 }
 

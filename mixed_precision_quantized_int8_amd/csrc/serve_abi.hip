@@ -392,23 +392,37 @@ i8l_status check_launch(const char* fn, int64_t rows, int64_t heads, int D) {
   return I8L_OK;
 }
 
+// Outputs of [rows][heads][D] elements do not overlap one another.
+i8l_status check_apart(const char* fn, const char* name, int64_t token_stride, int64_t head_stride,
+                       int64_t rows, int64_t heads, int D) {
+  const bool apart = (heads == 1 || head_stride >= D) && (rows == 1 || token_stride >= D) &&
+                     (heads == 1 || rows == 1 || token_stride >= (heads - 1) * head_stride + D ||
+                      head_stride >= (rows - 1) * token_stride + D);
+  if (!apart)
+    return fail(I8L_ERR_INVALID_ARG, fn, "%s: strides %lld, %lld make its heads overlap", name,
+                (long long)token_stride, (long long)head_stride);
+  return I8L_OK;
+}
+
 using Side = i8l::HeadArgs::Side;
 
-i8l_status check_heads(const char* fn, const i8l_heads* h, Side* out) {
+i8l_status check_heads(const char* fn, const i8l_heads* h, int64_t rows, int D, Side* out) {
   CHECK(check_count(fn, "heads", h->heads, 1, 65536));
   CHECK(check_rows(fn, "x", h->x, h->x_token_stride, h->x_head_stride));
   CHECK(check_rows(fn, "y", h->y, h->y_token_stride, h->y_head_stride));
+  CHECK(check_apart(fn, "y", h->y_token_stride, h->y_head_stride, rows, h->heads, D));
   if (h->weight) CHECK(check_ptr(fn, "weight", h->weight, 16));
   *out = Side{h->x, h->x_token_stride, h->x_head_stride, nullptr, 0, 0, h->y, h->y_token_stride,
               h->y_head_stride, h->weight, nullptr, h->heads};
   return I8L_OK;
 }
 
-i8l_status check_heads_grad(const char* fn, const i8l_heads_grad* h, int64_t rows, Side* out) {
+i8l_status check_heads_grad(const char* fn, const i8l_heads_grad* h, int64_t rows, int D, Side* out) {
   CHECK(check_count(fn, "heads", h->heads, 1, 65536));
   if (rows) {
     CHECK(check_rows(fn, "dy", h->dy, h->dy_token_stride, h->dy_head_stride));
     CHECK(check_rows(fn, "dx", h->dx, h->dx_token_stride, h->dx_head_stride));
+    CHECK(check_apart(fn, "dx", h->dx_token_stride, h->dx_head_stride, rows, h->heads, D));
     if (h->weight) CHECK(check_rows(fn, "x", h->x, h->x_token_stride, h->x_head_stride));
   }
   if (h->weight) {
@@ -436,8 +450,8 @@ I8L_API i8l_status int8_rotate_heads(const i8l_heads* q, const i8l_heads* k, int
   i8l::HeadArgs a{};
   CHECK(check_rotary(fn, rotary, head_dim, &a.turn));
   if (rows == 0) return ok();
-  CHECK(check_heads(fn, q, &a.side[0]));
-  if (k) CHECK(check_heads(fn, k, &a.side[1]));
+  CHECK(check_heads(fn, q, rows, head_dim, &a.side[0]));
+  if (k) CHECK(check_heads(fn, k, rows, head_dim, &a.side[1]));
   CHECK(check_launch(fn, rows, (int64_t)a.side[0].n + a.side[1].n, head_dim));
   CHECK_PTR(positions, 4);
   a.positions = positions;
@@ -469,8 +483,8 @@ I8L_API i8l_status int8_rotate_heads_backward(const i8l_heads_grad* q, const i8l
   CHECK(check_count(fn, "rows", rows, 0, INT32_MAX));
   i8l::HeadArgs a{};
   CHECK(check_rotary(fn, rotary, head_dim, &a.turn));
-  CHECK(check_heads_grad(fn, q, rows, &a.side[0]));
-  if (k) CHECK(check_heads_grad(fn, k, rows, &a.side[1]));
+  CHECK(check_heads_grad(fn, q, rows, head_dim, &a.side[0]));
+  if (k) CHECK(check_heads_grad(fn, k, rows, head_dim, &a.side[1]));
   CHECK(check_launch(fn, rows, (int64_t)a.side[0].n + a.side[1].n, head_dim));
   const bool weights = a.side[0].w || a.side[1].w;
   if (rows == 0 && !weights) return ok();
@@ -523,7 +537,7 @@ I8L_API i8l_status int8_cache_append(const i8l_kv_cache* cache, const i8l_sequen
   if (counts) CHECK_PTR(counts, 4);
   if (index) CHECK_PTR(index, 4);
   if (k_weight) CHECK_PTR(k_weight, 16);
-  if (q) CHECK(check_heads(fn, q, &a.side[0]));
+  if (q) CHECK(check_heads(fn, q, rows, c.D, &a.side[0]));
   const int64_t most = std::min(max_new, rows);
   // no sequence gets more tokens than its pages hold
   max_new = std::min(most, (int64_t)s.max_pages << c.ps);

@@ -317,6 +317,8 @@ def tree_plan(parents, lengths, cu=None, max_q=None, positions=None, masks=None)
     receive the results if given.
     """
     rows, n, max_q, dev, (pp, lp, cp) = _tree(parents, lengths, cu, max_q)
+    if masks is not None and (not isinstance(masks, torch.Tensor) or masks.dim() != 2):
+        raise ValueError("masks must be an int64 tensor [rows][words]")
     words = -(-max_q // 64) if masks is None else masks.shape[1]
     positions, op = _result(positions, torch.int32, (rows,), dev, "positions")
     masks, mp = _result(masks, torch.int64, (rows, words), dev, "masks")

@@ -45,7 +45,7 @@ def grad_struct(**kw):
 
 BAD_ROTARY = [dict(freqs=None), dict(freqs=P16 + 2), dict(pairs=-1), dict(pairs=33), dict(interleaved=2),
               dict(interleaved=-1), dict(factor=math.nan), dict(factor=math.inf)]
-BAD_HEADS = [dict(x=None), dict(x=P8), dict(y=None), dict(y=P8), dict(x_token_stride=4),
+BAD_HEADS = [dict(y_head_stride=56), dict(y_token_stride=0), dict(y_token_stride=248), dict(x=None), dict(x=P8), dict(y=None), dict(y=P8), dict(x_token_stride=4),
              dict(x_head_stride=-8), dict(y_token_stride=-8), dict(y_head_stride=12), dict(weight=P8),
              dict(heads=0), dict(heads=65537)]
 
@@ -69,6 +69,9 @@ def test_rotate_heads_refusals(i8l):
         assert call(q=heads_struct(**bad)) == INVALID, bad
         assert call(k=heads_struct(**bad)) == INVALID, bad
     assert call(rows=0, q=heads_struct(x=None)) == OK and i8l.last_error() == ""
+    # heads outside tokens do not overlap either (refused for the positions here)
+    assert call(q=heads_struct(y_token_stride=64, y_head_stride=128), pos=None) == INVALID
+    assert "positions" in i8l.last_error()
     assert call(rows=0, rot=rotary_struct(pairs=0, freqs=None)) == OK
 
 
@@ -89,7 +92,8 @@ def test_rotate_heads_backward_refusals(i8l):
         assert call(rot=rotary_struct(**bad)) == INVALID, bad
     for bad in (dict(dy=None), dict(dy=P8), dict(dx=None), dict(x=None), dict(x=P8), dict(weight=P8),
                 dict(dweight=None), dict(dweight=P16 + 1), dict(heads=0), dict(dy_token_stride=3),
-                dict(x_head_stride=-8), dict(dx_token_stride=4)):
+                dict(x_head_stride=-8), dict(dx_token_stride=4), dict(dx_head_stride=0),
+                dict(dx_token_stride=128)):
         assert call(q=grad_struct(**bad)) == INVALID, bad
         assert call(k=grad_struct(**bad)) == INVALID, bad
     assert L.int8_rotate_heads_backward(None, None, 64, 2, P16, ref(rotary_struct()), 1e-6, 0, None, 0,
@@ -128,7 +132,7 @@ def test_cache_append_refusals(i8l):
     most = 2046 * 16 + 16
     assert call(cache=c, seqs=s, rows=most, kv_rows=most, most=most) == INVALID
     assert "too many" in i8l.last_error()
-    assert call(seqs=s, rows=1 << 27, kv_rows=1 << 27, most=1 << 27, q=heads_struct(heads=64)) == INVALID
+    assert call(seqs=s, rows=1 << 27, kv_rows=1 << 27, most=1 << 27, q=heads_struct(heads=64, y_token_stride=4096)) == INVALID
     assert "too many" in i8l.last_error()
 
 

@@ -103,6 +103,8 @@ def test_rotate_heads(lib, T, Hq, Hk, D, pairs, inter, dtype):
     same(x, a)
     same(y, b)
     assert bool((wide[:, -1] == 7).all()) and bool((wide[:, :, D:] == 7).all())
+    heads_first = torch.empty((Hq, T, D), dtype=dt, device="cuda").transpose(0, 1)
+    same(lib.rotate_heads(qd, pd, rot, q_weight=qw.cuda(), eps=1e-5, q_out=heads_first), a)
     lib.rotate_heads(qd, pd, rot, k=kd, q_weight=qw.cuda(), eps=1e-5, q_out=qd, k_out=kd)
     same(qd, a)
     same(kd, b)
