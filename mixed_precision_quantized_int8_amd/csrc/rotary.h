@@ -92,8 +92,10 @@ struct Angles {
       const int i = pair(r, j, e);
       float2 a = make_float2(1.0f, 0.0f);
       if (r.pairs) a = get(max(i, 0), e);   // uniform
-      c[e] = i < 0 ? 1.0f : a.x;
-      s[e] = i < 0 ? 0.0f : back ? -a.y : a.y;
+      // (halves: a lane turns all of its places or none, which turn() settles)
+      const bool on = LAYOUT == kTurnHalves || i >= 0;
+      c[e] = on ? a.x : 1.0f;
+      s[e] = !on ? 0.0f : back ? -a.y : a.y;
       if (LAYOUT == kTurnOdd && 16 * j + e < r.pairs) s[e] = -s[e];   // y_a = a c + b (-s), y_b = b c + a s
     }
   }
