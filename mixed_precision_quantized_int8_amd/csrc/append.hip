@@ -10,7 +10,7 @@
 //
 // Bound by HBM and, for the keys, by the vector unit: every head forms its own angles.
 // 24.8 thousand tokens of four sequences, bf16, 32 query heads on 8 of 128, norms on
-// both: 560 MB in 133 us, 4.2 TB/s (the queries alone 80 us, 5.1 TB/s; keys and values 63,
+// both: 560 MB in 132 us, 4.2 TB/s (the queries alone 79 us, 5.1 TB/s; keys and values 62,
 // as cache_write without turning 38).  One token each of 16 sequences: 6 us, latency.
 #include "pages.h"
 #include "rotary.h"
@@ -70,7 +70,7 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   if (g < full) {
     const int page = s.table[(size_t)b * s.max_pages + g];
     const bool page_ok = page >= 0 && page < c.n_pages;
-    // A token at a time, the next one's elements on their way; what is turned waits in LDS
+    // A token at a time, the next two's elements on their way; what is turned waits in LDS
     // for the page's maximum (a thread reads back what it wrote).
     const auto load = [&](int u, v4u (&p)[2]) {
       const int tok = (t + u * BS) / lanes, pos = (g << ps) + tok;
@@ -87,12 +87,15 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
     };
     // magnitudes of both types are in the order of their bits, infinities and NaNs last
     u16x2 mag = {0, 0};
-    v4u next[2];
+    v4u next[2], after[2];
     load(0, next);
+    load(1, after);
 #pragma unroll 1
     for (int u = 0; u < NT; ++u) {
       v4u p[2] = {next[0], next[1]};
-      if (u + 1 < NT) load(u + 1, next);
+      next[0] = after[0];
+      next[1] = after[1];
+      if (u + 2 < NT) load(u + 2, after);
       const int pos = (g << ps) + (t + u * BS) / lanes;
       v4u q[2] = {p[0], p[1]};
       turned(q, pos);
@@ -163,7 +166,7 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   }
 }
 
-// (80 registers, for six waves a SIMD: 24.8 k tokens, 32 heads on 8, 133 us, with 93
+// (80 registers, for six waves a SIMD: 24.8 k tokens, 32 heads on 8, 132 us, with 93
 // registers 137; keys kept in registers as values are, 126 of them, 148.  Halves through
 // LDS do not fit.)
 template <bool BF, int LAYOUT, int BS, int NU>
