@@ -42,7 +42,7 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   // frequencies come from the cache for each token: kept, their registers would cost waves.
   auto turned = [&](v4u (&p)[2], int pos) {
     int zero = 0;
-    asm volatile("" : "+s"(zero));
+    if (LAYOUT != kTurnOdd) asm volatile("" : "+s"(zero));   // (halves through LDS have few waves anyway)
     float y[16], freq[Angles<LAYOUT>::N];
     v4u w[2];
 #pragma unroll
