@@ -62,11 +62,12 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int b) {
   return r;
 }
 
-// Position of query qi of a sequence.  (A tree's matter for a window or a bias only.)
+// Position of query qi of a sequence.  (A tree's matter for a window or a bias only; its
+// distances stay in 32 bits.)
 template <bool TREE>
 __device__ __forceinline__ int position(const ArgsOf<TREE>& a, const Rows& sq, int qi) {
   if constexpr (TREE)
-    return a.positions ? min(max(a.positions[sq.c0 + qi], -(1 << 30)), 1 << 30) : sq.len;
+    return a.positions ? min(max(a.positions[sq.c0 + qi], -(1 << 29)), 1 << 30) : sq.len;
   else return sq.first_pos + qi;
 }
 // Which of the drafts 64 w .. 64 w + 63 query qi's mask names, of the sequence's n.

@@ -280,6 +280,47 @@ def test_rotate_heads_module(lib):
                for p in (qkv.weight16, qkv.bias, m.q_weight, m.k_weight))
 
 
+def test_rotate_heads_module_in_a_graph(lib):
+    """A training step's forward and backward pass of RotateHeads, captured and replayed with
+    new contents, eager work between: every replay against eager, on another stream too."""
+    from mixed_precision_quantized_int8_amd.module import RotateHeads
+
+    g = gen(3)
+    T, H, D = 700, 6, 64
+    m = RotateHeads(D, lib.rotary(D), dtype=torch.bfloat16)
+    q, k = (torch.randn((T, h, D), generator=g).bfloat16().cuda().requires_grad_() for h in (H, 2))
+    dy = [torch.randn((T, h, D), generator=g).bfloat16().cuda() for h in (H, 2)]
+    pos = torch.randint(0, 1 << 18, (T,), generator=g).to(torch.int32).cuda()
+
+    def step():
+        out = m(q, pos, k)
+        return list(out) + list(torch.autograd.grad(out, (q, k, m.q_weight, m.k_weight), dy))
+
+    def eager():
+        return [t.detach().clone() for t in step()]      # (no graph of these leaves lives on)
+
+    want = eager()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for a, b in zip(eager(), want):
+            same(a, b)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [t.detach() for t in step()]
+    for i in range(3):
+        with torch.no_grad():
+            q.copy_(torch.randn(q.shape, generator=g).bfloat16())
+            m.k_weight.copy_((1 + 0.2 * torch.randn(D, generator=g)).bfloat16())
+        dy[0].copy_(torch.randn(dy[0].shape, generator=g).bfloat16())
+        want = eager()
+        torch.cuda.synchronize()
+        graph.replay()
+        for a, b in zip(held, want):
+            same(a, b, f"replay {i}")
+
+
 # ---- into the cache -----------------------------------------------------------------
 
 
@@ -417,6 +458,66 @@ def test_cache_append_picks_rows(lib, turned):
                      counts=ints([50, 1, -3]), index=torch.cat([index[:2], index[10:11], index[3:]]).cuda())
     for x, y in zip(parts_of(a), parts_of(b)):
         same(y, x)
+
+
+def test_cache_append_counts_and_queries(lib):
+    """counts with queries: the first rows of each sequence, the others left as they are."""
+    g = gen(6)
+    H, G, D, P = 2, 3, 64, 16
+    rot, w = lib.rotary(D, interleaved=True), (1 + 0.3 * torch.randn(D, generator=g)).half().cuda()
+    a, b = (blank_cache(lib, 9, 3, H, D, P, torch.float16) for _ in range(2))
+    table = torch.arange(9).view(3, 3).to(torch.int32).cuda()
+    q, k, v = torch.randn((40, H * (G + 2), D), generator=g).half().cuda().split([H * G, H, H], dim=1)
+    counts, first = [7, 0, 18], [0, 10, 20]
+    lens = [20, 5, 18]
+    rows = torch.cat([torch.arange(f, f + n) for f, n in zip(first, counts)]).cuda()
+    q1 = lib.cache_append(a, k[rows], v[rows], table, ints(lens), q=q[rows], rotary=rot, q_weight=w, k_weight=w,
+                          cu=cu_of(counts))
+    out = torch.full((40, H * G, D), 9.0, dtype=torch.float16, device="cuda")
+    lib.cache_append(b, k, v, table, ints(lens), q=q, rotary=rot, q_weight=w, k_weight=w,
+                     cu=ints([0, 10, 20, 40]), counts=ints(counts), q_out=out)
+    same(out[rows], q1)
+    left = torch.ones(40, dtype=torch.bool, device="cuda")
+    left[rows] = False
+    assert bool((out[left] == 9).all())
+    for x, y in zip(parts_of(a), parts_of(b)):
+        same(y, x)
+
+
+@pytest.mark.parametrize("n", [64, 65, 300])
+def test_tree_attention_of_many_sequences(lib, n):
+    """As many sequences as a share's plan holds, and more."""
+    g = gen(n)
+    H, G, D, P, dt = 1, 8, 64, 32, torch.float16
+    lens = [2100] + torch.randint(0, 90, (n - 1,), generator=g).tolist()
+    sizes = [40] + torch.randint(0, 6, (n - 1,), generator=g).tolist()
+    cache, table, slots, kv = filled_cache(lib, lens, H, D, P, dt, g, poison=True)
+    q, k, v = torch.randn((sum(sizes), H * (G + 2), D), generator=g).to(dt).cuda().split([H * G, H, H], dim=1)
+    positions, seen = [], []
+    for m, size in zip(lens, sizes):
+        p, s = O.tree_plan(random_tree(size, g), m)
+        positions += p
+        seen.append(s)
+    masks = torch.cat([O.words(s, 1) for s in seen if s]).cuda()
+    got = lib.tree_attention(q, k, v, cache, table, ints(lens), masks, cu=cu_of(sizes), slots=slots,
+                             max_q=40, max_len=2100, scale=0.15)
+    check_tree(lib, cache, table, slots, kv, lens, None, q, k, v, P, dt, 0.15, 0, None, got, positions, seen)
+
+
+def test_tree_attention_positions_anywhere(lib):
+    """Positions at the ends of 32 bits: no key, or all of them, in a window."""
+    g = gen(12)
+    H, G, D, P, n, dt = 1, 8, 64, 16, 50, torch.float16
+    for m in (2, 30):
+        cache, table, slots, kv = filled_cache(lib, [n], H, D, P, dt, g)
+        q, k, v = torch.randn((m, H * (G + 2), D), generator=g).to(dt).cuda().split([H * G, H, H], dim=1)
+        positions = [2 ** 31 - 1, -2 ** 31] * (m // 2)
+        masks = torch.full((m, 1), (1 << m) - 1, dtype=torch.int64, device="cuda")
+        got = lib.tree_attention(q, k, v, cache, table, ints([n]), masks, positions=ints(positions), cu=ints([0, m]),
+                                 slots=slots, max_q=m, scale=0.2, window=9)
+        at = [2 ** 30, -2 ** 29] * (m // 2)           # as the kernels take them
+        check_tree(lib, cache, table, slots, kv, [n], None, q, k, v, P, dt, 0.2, 9, None, got, at,
+                   [[set(range(m))] * m])
 
 
 # ---- trees --------------------------------------------------------------------------
