@@ -42,12 +42,13 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   // frequencies come from the cache for each token: kept, their registers would cost waves.
   auto turned = [&](v4u (&p)[2], int pos) {
     int zero = 0;
-    if (LAYOUT != kTurnOdd) asm volatile("" : "+s"(zero));   // (halves through LDS have few waves anyway)
+    asm volatile("" : "+s"(zero));
     float y[16], freq[Angles<LAYOUT>::N];
     v4u w[2];
+    if (LAYOUT != kTurnOdd)
 #pragma unroll
-    for (int e = 0; e < Angles<LAYOUT>::N; ++e)
-      freq[e] = a.turn.pairs ? a.turn.freqs[zero + max(Angles<LAYOUT>::pair(a.turn, j, e), 0)] : 0.0f;
+      for (int e = 0; e < Angles<LAYOUT>::N; ++e)
+        freq[e] = a.turn.pairs ? a.turn.freqs[zero + max(Angles<LAYOUT>::pair(a.turn, j, e), 0)] : 0.0f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       w[r] = v4u{0, 0, 0, 0};
@@ -63,7 +64,8 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
       for (int e = 0; e < 16; ++e) y[e] *= wf[e];
     }
     Angles<LAYOUT> angles;
-    angles_at(angles, a.turn, j, pos, freq);
+    if constexpr (LAYOUT == kTurnOdd) odd_angles_at(angles, a.turn, lanes, j, pos, row, lane);
+    else angles_at(angles, a.turn, j, pos, freq);
     turn<LAYOUT>(y, angles, a.turn, j, row, lane);
     pack<BF>(y, p);
   };

@@ -119,9 +119,24 @@ __device__ __forceinline__ void angles_at(Angles<LAYOUT>& a, const Turn& r, int 
   a.of(r, j, false, [&](int, int e) { return turned_by(u[e], r.factor); });
 }
 
+// The same for kTurnOdd, where both lanes of a pair need its angle: a head's lanes form
+// each of them once and pass them through `row`, the wave's part of LDS.
+constexpr int kTurnRow = 64 * 17;   // floats a wave: 64 / lanes * pairs angles, or a lane's 16
+                                    // elements and one that shifts the banks
+__device__ __forceinline__ void odd_angles_at(Angles<kTurnOdd>& a, const Turn& r, int lanes, int j, int pos,
+                                              float* row, int lane) {
+  float2* head = reinterpret_cast<float2*>(row) + lane / lanes * r.pairs;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  for (int q = j; q < r.pairs; q += lanes) head[q] = angle(pos, r.freqs[q], r.factor);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  a.of(r, j, false, [&](int i, int) { return head[i]; });
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // x turned in place: x[8 r + e] is element e of run r.  kTurnOdd: `row` is this wave's
 // kTurnRow floats of LDS.
-constexpr int kTurnRow = 64 * 17;   // (a lane's 16 elements, and one that shifts the banks)
 template <int LAYOUT>
 __device__ __forceinline__ void turn(float (&x)[16], const Angles<LAYOUT>& a, const Turn& r, int j,
                                      float* row, int lane) {
