@@ -139,6 +139,13 @@ class Int8Linear(torch.nn.Module):
                 f"threshold={self.threshold}")
 
 
+def _whole(g):
+    """A gradient as the library takes it: dense, from a multiple of 16 bytes on (autograd
+    hands on views that start anywhere)."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class _RotateHeadsFn(torch.autograd.Function):
     """(q', k') of rotate_heads, with its gradients (first order)."""
 
@@ -156,8 +163,8 @@ class _RotateHeadsFn(torch.autograd.Function):
     def backward(ctx, *grads):
         positions, q, k, q_weight, k_weight = ctx.saved_tensors
         dq, dk, dqw, dkw = _rotate_heads_backward(
-            grads[0].contiguous(), positions, ctx.rotary, q=q,
-            dk=grads[1].contiguous() if ctx.two else None, k=k, q_weight=q_weight, k_weight=k_weight,
+            _whole(grads[0]), positions, ctx.rotary, q=q,
+            dk=_whole(grads[1]) if ctx.two else None, k=k, q_weight=q_weight, k_weight=k_weight,
             eps=ctx.eps)
         return dq, dk, None, None, dqw, dkw, None
 

@@ -877,3 +877,28 @@ def test_wrappers_refuse_on_the_gpu(lib):
         lib.tree_plan(pos, lens[:3])
     with pytest.raises(TypeError):
         lib.tree_accept(pos, pos, pos, lens)
+
+
+def test_gradients_that_start_anywhere(lib):
+    """A gradient that autograd hands on as a view (of a concatenation's, say) may start at any
+    element, or have strides of 0."""
+    from mixed_precision_quantized_int8_amd.module import RotateHeads
+
+    g = gen(5)
+    T, H, D = 7, 3, 64
+    m = RotateHeads(D, lib.rotary(D))
+    q, k = (torch.randn((T, h, D), generator=g).half().cuda().requires_grad_() for h in (H, 1))
+    pos, odd = ints(list(range(T))), torch.zeros(3, dtype=torch.float16, device="cuda")
+    w = torch.randn(3 + T * (H + 1) * D, generator=g).half().cuda()
+    a, b = m(q, pos, k)
+    torch.cat([odd, a.flatten(), b.flatten()]).backward(w)
+    got = [q.grad, k.grad, m.q_weight.grad, m.k_weight.grad]
+    n = T * H * D
+    want = lib.rotate_heads_backward(w[3:3 + n].view(T, H, D).clone(), pos, m.rotary, q=q.detach(),
+                                     dk=w[3 + n:].view(T, 1, D).clone(), k=k.detach(),
+                                     q_weight=m.q_weight.detach(), k_weight=m.k_weight.detach())
+    for x, y in zip(got, want):
+        same(x, y)
+    dq = torch.autograd.grad(m(q, pos).sum(), q)[0]
+    same(dq, lib.rotate_heads_backward(torch.ones_like(q), pos, m.rotary, q=q.detach(),
+                                       q_weight=m.q_weight.detach())[0])
