@@ -120,7 +120,7 @@ class Int8DecoderLayer(torch.nn.Module):
             else:
                 cache_write(cache, k, v, page_table, lengths, cu=cu, slots=slots, max_new=max_q)
             a = cache_attention(q, cache, page_table, lengths, cu=cu, slots=slots, max_q=max_q,
-                                max_len=max_len, window=window, alibi=self.alibi)
+                                max_len=max_len, window=window, alibi=self.alibi, out=self._answers(q, cu))
             return self._rest(a, r)
 
     def draft(self, x, residual, cache, page_table, lengths, positions, masks, cu=None, slots=None,
@@ -137,7 +137,7 @@ class Int8DecoderLayer(torch.nn.Module):
                                     k_weight=self.k_norm, eps=self.head_eps, q_out=q, k_out=k)
             a = tree_attention(q, k, v, cache, page_table, lengths, masks, positions=positions, cu=cu,
                                slots=slots, max_q=max_q, max_len=max_len, window=window,
-                               alibi=self.alibi)
+                               alibi=self.alibi, out=self._answers(q, cu))
             return (*self._rest(a, r), (k, v))
 
     def accept(self, kv, cache, page_table, lengths, path, counts, cu=None, slots=None, max_new=None):
@@ -152,6 +152,11 @@ class Int8DecoderLayer(torch.nn.Module):
         qkv, r = self._norm_product(self.qkv, x, residual, self.norm1)
         qkv = qkv.view(x.shape[0], H + 2 * self.kv_heads, D)
         return qkv[:, :H], qkv[:, H:H + self.kv_heads], qkv[:, H + self.kv_heads:], r
+
+    def _answers(self, q, cu):
+        """Where attention writes.  With cu there may be rows that it leaves as they are; the
+        next product's outlier columns are those of all of its rows, so these hold 0."""
+        return None if cu is None else q.new_zeros(q.shape)
 
     def _rest(self, a, r):
         """(y, r') from the attention's output on."""

@@ -166,3 +166,36 @@ def test_norms_without_a_rotation_and_biases_with_one(lib):
     assert torch.equal(outs[0], outs[1])
     assert bool(outs[2].isfinite().all()) and not torch.equal(outs[2], outs[0])
     close(outs[0], reference(p, x, torch.zeros(0), False, w, None)[0], "norm of the queries alone")
+
+
+@pytest.mark.parametrize("draft", [False, True])
+def test_rows_behind_the_sequences(lib, monkeypatch, draft):
+    """What memory held where attention answers nothing (rows behind the last sequence,
+    drafts past max_q) is not seen by the product after it, whose outlier columns are those
+    of all of its rows."""
+    import mixed_precision_quantized_int8_amd.decoder as decoder
+
+    p, g = parts(10), torch.Generator().manual_seed(11)
+    layer = decoder.Int8DecoderLayer(*p, heads=HEADS, kv_heads=KV, rotary=lib.rotary(D))
+    n, lens = [5, 3], ints([20, 9])
+    table, cu = ints([[0, 1], [3, 2]]), ints([0, 5, 8])
+    x = torch.randn((12, HIDDEN), generator=g).half().cuda()
+    positions, masks = lib.tree_plan(ints([-1, 0, 0, 1, 2, -1, 0, 1, 0, 0, 0, 0]), lens, cu=cu, max_q=5)
+    positions[8:] = 0                                        # (as the plan left them)
+    name = "tree_attention" if draft else "cache_attention"
+    attention, outs = getattr(decoder, name), []
+    for held in (0.0, 1000.0):
+        def filled(q, *a, out=None, **kw):
+            out = torch.full(q.shape, held, dtype=q.dtype, device=q.device) if out is None else out
+            return attention(q, *a, out=out, **kw)
+
+        monkeypatch.setattr(decoder, name, filled)
+        cache = lib.new_cache(4, 2, KV, D, page_size=16)
+        for t in (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, cache.k_tail, cache.v_tail):
+            t.zero_()
+        if draft:
+            outs.append(layer.draft(x, None, cache, table, lens, positions, masks, cu, max_q=4, max_len=32)[:2])
+        else:
+            outs.append(layer(x, None, cache, table, lens, cu, max_q=5, max_len=32))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
