@@ -71,8 +71,9 @@ __device__ __forceinline__ float2 angle(int pos, float freq, float f) {
 }
 
 // The 8 (kTurnOdd: 16) angles of a thread, from get(i, e), pair i's cos and sin for place
-// e; a place past the pairs has angle 0 and factor 1 (its i is 0: no branch, so that what
-// get loads is on its way together).  `back`: the other way.
+// e; a place past the pairs has pair 0's (no branch, so that what get loads is on its way
+// together), which turn() does not use, or for kTurnOdd what keeps its element there: 1 and
+// -0.  `back`: the other way.
 template <int LAYOUT>
 struct Angles {
   static constexpr int N = LAYOUT == kTurnOdd ? 16 : 8;
@@ -92,10 +93,9 @@ struct Angles {
       const int i = pair(r, j, e);
       float2 a = make_float2(1.0f, 0.0f);
       if (r.pairs) a = get(max(i, 0), e);   // uniform
-      // (halves: a lane turns all of its places or none, which turn() settles)
-      const bool on = LAYOUT == kTurnHalves || i >= 0;
+      const bool on = LAYOUT != kTurnOdd || i >= 0;
       c[e] = on ? a.x : 1.0f;
-      s[e] = !on ? 0.0f : back ? -a.y : a.y;
+      s[e] = !on ? -0.0f : back ? -a.y : a.y;
       if (LAYOUT == kTurnOdd && 16 * j + e < r.pairs) s[e] = -s[e];   // y_a = a c + b (-s), y_b = b c + a s
     }
   }
@@ -122,7 +122,7 @@ __device__ __forceinline__ void angles_at(Angles<LAYOUT>& a, const Turn& r, int 
 // The same for kTurnOdd, where both lanes of a pair need its angle: a head's lanes form
 // each of them once and pass them through `row`, the wave's part of LDS.
 constexpr int kTurnRow = 64 * 17;   // floats a wave: 64 / lanes * pairs angles, or a lane's 16
-                                    // elements and one that shifts the banks
+                                    // elements and a 0, which also shifts the banks
 __device__ __forceinline__ void odd_angles_at(Angles<kTurnOdd>& a, const Turn& r, int lanes, int j, int pos,
                                               float* row, int lane) {
   float2* head = reinterpret_cast<float2*>(row) + lane / lanes * r.pairs;
@@ -135,8 +135,11 @@ __device__ __forceinline__ void odd_angles_at(Angles<kTurnOdd>& a, const Turn& r
   __builtin_amdgcn_wave_barrier();
 }
 
-// x turned in place: x[8 r + e] is element e of run r.  kTurnOdd: `row` is this wave's
-// kTurnRow floats of LDS.
+// x turned in place: x[8 r + e] is element e of run r.  What has no pair is kept, not turned
+// by 0: with an infinite neighbour it would become a NaN.  kTurnOdd: `row` is this wave's
+// kTurnRow floats of LDS; what has no pair meets a 0 there, and x 1 + 0 (-0) is x, zeros and
+// infinities too (selects at the end instead: 8192 tokens with a quarter of 80 turned 44 us,
+// so 41).
 template <int LAYOUT>
 __device__ __forceinline__ void turn(float (&x)[16], const Angles<LAYOUT>& a, const Turn& r, int j,
                                      float* row, int lane) {
@@ -153,8 +156,9 @@ __device__ __forceinline__ void turn(float (&x)[16], const Angles<LAYOUT>& a, co
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float p = x[2 * e], q = x[2 * e + 1];
-      x[2 * e] = __builtin_fmaf(p, a.c[e], -(q * a.s[e]));
-      x[2 * e + 1] = __builtin_fmaf(p, a.s[e], q * a.c[e]);
+      const bool on = 8 * j + e < r.pairs;
+      x[2 * e] = on ? __builtin_fmaf(p, a.c[e], -(q * a.s[e])) : p;
+      x[2 * e + 1] = on ? __builtin_fmaf(p, a.s[e], q * a.c[e]) : q;
     }
   } else {
     // (a wave's LDS accesses are done in order; no other wave uses this part)
@@ -162,14 +166,16 @@ __device__ __forceinline__ void turn(float (&x)[16], const Angles<LAYOUT>& a, co
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int e = 0; e < 16; ++e) mine[e] = x[e];
+    mine[16] = 0.0f;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const float* head = mine - 17 * j;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int d = 16 * j + e;
-      const int other = d < r.pairs ? d + r.pairs : d < 2 * r.pairs ? d - r.pairs : d;
-      x[e] = __builtin_fmaf(x[e], a.c[e], head[other + (other >> 4)] * a.s[e]);
+      const int other = d < r.pairs ? d + r.pairs : d - r.pairs;
+      const int at = d < 2 * r.pairs ? other + (other >> 4) : 17 * j + 16;
+      x[e] = __builtin_fmaf(x[e], a.c[e], head[at] * a.s[e]);
     }
     __builtin_amdgcn_wave_barrier();
   }

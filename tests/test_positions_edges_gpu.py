@@ -1,0 +1,83 @@
+"""Rotary positions and drafts on the GPU where a call's inputs are unusual: what stays as it
+is beside infinities and NaNs."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_positions_gpu import (blank_cache, cu_of, freqs_of, gen, ints, lib, parts_of,  # noqa: E402, F401
+                                positions_of, say, within)
+from oracle import positions_oracle as O  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+def bits(x):
+    """The bits of a 16-bit tensor, one pattern for every NaN."""
+    x = x.cpu().contiguous()
+    return torch.where(x.isnan(), torch.tensor(0x7fff, dtype=torch.int16), x.view(torch.int16))
+
+
+def same_bits(a, b, what=""):
+    eq = bits(a) == bits(b)
+    assert bool(eq.all()), f"{what}: {int((~eq).sum())} of {eq.numel()} differ"
+
+
+# D, pairs, interleaved: aligned halves, pairs, halves through LDS; a part that ends at a
+# lane's first element, inside a lane, at its last but one; nothing turned
+PARTS = [(64, 16, False), (64, 8, True), (64, 11, True), (80, 10, False), (80, 10, True), (128, 1, False),
+         (128, 1, True), (96, 36, False), (96, 47, False), (256, 100, False), (256, 100, True), (64, 0, True),
+         (64, 0, False)]
+
+
+def odd_heads(T, H, D, pairs, dt, g):
+    """Heads whose elements past the turned ones are any: infinities, NaNs and zeros of both
+    signs beside finite ones, in every place of some head."""
+    x = torch.randn((T, H, D), generator=g).to(dt)
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -0.0, 0.0])
+    at = torch.randint(0, 9, (T, H, D), generator=g)
+    at[..., :2 * pairs] = 9
+    for i, v in enumerate(odd):
+        x[at == i] = float(v)
+    return x
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D,pairs,inter", PARTS)
+def test_what_does_not_turn_stays(lib, D, pairs, inter, dtype):  # noqa: F811
+    """Elements past the turned ones come out bit for bit, whatever they and their neighbours
+    are, and change nothing among the turned ones: forward and backward."""
+    say("what does not turn", D, pairs, inter, dtype)
+    dt, g = TYPES[dtype], gen(D + pairs)
+    T, H = 40, 3
+    x = odd_heads(T, H, D, pairs, dt, g)
+    clean = x.clone()
+    clean[..., 2 * pairs:] = 1
+    f, pos = freqs_of(pairs), torch.randint(0, 1 << 18, (T,), generator=g).to(torch.int32)
+    rot = lib.Rotary(f.cuda(), interleaved=inter, factor=1.25)
+    for y, (want, tol) in (
+            (lib.rotate_heads(x.cuda(), pos.cuda(), rot), O.rotate(clean, pos, f, inter, 1.25)),
+            (lib.rotate_heads_backward(x.cuda(), pos.cuda(), rot)[0],
+             O.rotate_grad(clean, None, pos, f, inter, 1.25)[0])):
+        same_bits(y[..., 2 * pairs:], x[..., 2 * pairs:], "what does not turn")
+        n = 2 * pairs
+        within(y[..., :n], want[..., :n], tol[..., :n], "what turns")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D,pairs,inter", PARTS)
+def test_what_does_not_turn_reaches_the_cache(lib, D, pairs, inter, dtype):  # noqa: F811
+    """cache_append: queries, and keys in the incomplete page, the same."""
+    say("what does not turn, appended", D, pairs, inter, dtype)
+    dt, g = TYPES[dtype], gen(D + pairs + 1)
+    P, H, n = 64, 2, 37
+    c = blank_cache(lib, 1, 1, H, D, P, dt)
+    q, k = odd_heads(n, 3, D, pairs, dt, g), odd_heads(n, H, D, pairs, dt, g)
+    v = torch.randn((n, H, D), generator=g).to(dt)
+    rot = lib.Rotary(freqs_of(pairs).cuda(), interleaved=inter)
+    got = lib.cache_append(c, k.cuda(), v.cuda(), ints([[0]]), ints([n]), q=q.cuda(), rotary=rot, cu=ints([0, n]))
+    same_bits(got[..., 2 * pairs:], q[..., 2 * pairs:], "queries")
+    same_bits(c.k_tail[0].transpose(0, 1)[:n, :, 2 * pairs:], k[..., 2 * pairs:], "keys")
