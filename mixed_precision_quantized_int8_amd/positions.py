@@ -50,7 +50,8 @@ class Rotary:
     ``freqs`` fp32 [pairs] on the GPU (``rotary`` makes the usual ones); the pairs are
     elements (i, i + pairs), or (2 i, 2 i + 1) if ``interleaved``; elements from 2 * pairs
     on stay as they are.  ``factor`` multiplies what turns.  It holds the tensor's address:
-    its attributes do not change, and the tensor must not be given other storage.
+    its attributes do not change, and the tensor must not be given other storage.  A copy
+    (copy.copy: over the same tensor; deepcopy, pickle: over one of its own) holds its own.
     """
 
     __slots__ = ("freqs", "interleaved", "factor", "device", "_struct")
@@ -72,6 +73,9 @@ class Rotary:
 
     def __delattr__(self, name):
         raise AttributeError(f"{name}: a Rotary does not change")
+
+    def __reduce__(self):
+        return type(self), (self.freqs, self.interleaved, self.factor)
 
 
 # what the constructor writes an unchanging object's attributes with
