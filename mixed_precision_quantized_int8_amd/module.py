@@ -154,16 +154,20 @@ class _RotateHeadsFn(torch.autograd.Function):
         out = _rotate_heads(q, positions, rotary, k=k, q_weight=q_weight, k_weight=k_weight, eps=eps)
         # without a norm the gradient does not depend on what went in
         ctx.save_for_backward(positions, q if q_weight is not None else None,
-                              k if k_weight is not None else None, q_weight, k_weight)
+                              k if k_weight is not None else None, q_weight, k_weight,
+                              None if rotary is None else rotary.freqs)
         ctx.rotary, ctx.eps, ctx.two = rotary, eps, k is not None
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, *grads):
-        positions, q, k, q_weight, k_weight = ctx.saved_tensors
+        positions, q, k, q_weight, k_weight, freqs = ctx.saved_tensors
+        rotary = ctx.rotary
+        if rotary is not None and freqs.data_ptr() != rotary.freqs.data_ptr():   # (kept elsewhere by a hook)
+            rotary = type(rotary)(freqs, rotary.interleaved, rotary.factor)
         dq, dk, dqw, dkw = _rotate_heads_backward(
-            _whole(grads[0]), positions, ctx.rotary, q=q,
+            _whole(grads[0]), positions, rotary, q=q,
             dk=_whole(grads[1]) if ctx.two else None, k=k, q_weight=q_weight, k_weight=k_weight,
             eps=ctx.eps)
         return dq, dk, None, None, dqw, dkw, None

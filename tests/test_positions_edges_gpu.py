@@ -81,3 +81,28 @@ def test_what_does_not_turn_reaches_the_cache(lib, D, pairs, inter, dtype):  # n
     got = lib.cache_append(c, k.cuda(), v.cuda(), ints([[0]]), ints([n]), q=q.cuda(), rotary=rot, cu=ints([0, n]))
     same_bits(got[..., 2 * pairs:], q[..., 2 * pairs:], "queries")
     same_bits(c.k_tail[0].transpose(0, 1)[:n, :, 2 * pairs:], k[..., 2 * pairs:], "keys")
+
+
+def test_frequencies_changed_before_the_backward_pass(lib):  # noqa: F811
+    """Frequencies written over between the passes would give another function's gradient:
+    autograd says so, as for any tensor that a backward pass needs."""
+    from mixed_precision_quantized_int8_amd.module import RotateHeads
+
+    m = RotateHeads(64, lib.rotary(64))
+    q = torch.randn((5, 2, 64), generator=gen(1)).half().cuda().requires_grad_()
+    pos = ints(list(range(5)))
+    out = m(q, pos)
+    m.rotary.freqs.mul_(0.5)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    m(q, pos).sum().backward()                    # (with the new ones from here on)
+    want, _, dw, _ = lib.rotate_heads_backward(torch.ones_like(q), pos, m.rotary, q=q.detach(),
+                                               q_weight=m.q_weight.detach())
+    same_bits(q.grad, want)
+    same_bits(m.q_weight.grad, dw)
+    with torch.autograd.graph.save_on_cpu():      # what was saved is what counts
+        out = m(q, pos)
+    m.rotary.freqs.mul_(0.5)
+    same_bits(torch.autograd.grad(out.sum(), q)[0], want)
+    plain = RotateHeads(64, None)                 # no rotation: nothing to change
+    torch.autograd.grad(plain(q, pos).sum(), q)
