@@ -222,8 +222,9 @@ def rotate_heads_backward(dq, positions, rotary=None, q=None, dk=None, k=None, q
     q and k, the forward pass's inputs, are needed where there is a weight.  Weight
     gradients are summed over rows and heads in a fixed order.  ``dq_out`` and ``dk_out``
     (which may be dq and dk) receive the results if given; ``workspace`` (uint8,
-    ``rotate_heads_workspace_bytes``): None allocates it.
+    ``rotate_heads_workspace_bytes``): None allocates it.  It has no gradient of its own.
     """
+    _inference(dq, q, dk, k, q_weight, k_weight)
     code = _half_type(dq, "dq", 3)
     rows, H, D = dq.shape
     dev, dt = dq.device, dq.dtype
