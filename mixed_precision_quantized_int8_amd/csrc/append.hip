@@ -12,6 +12,8 @@
 // 24.8 thousand tokens of four sequences, bf16, 32 query heads on 8 of 128, norms on
 // both: 560 MB in 132 us, 4.2 TB/s (the queries alone 79 us, 5.1 TB/s; keys and values 62,
 // as cache_write without turning 38).  One token each of 16 sequences: 6 us, latency.
+#include <algorithm>
+
 #include "pages.h"
 #include "rotary.h"
 
@@ -208,9 +210,11 @@ namespace {
 template <bool BF, int LAYOUT, int BS, int NU>
 void launch_sized(const Cache& c, const Sequences& s, const CacheRows& x, const HeadArgs& a,
                   const uint16_t* k_w, uint32_t page_blocks, int max_q, hipStream_t stream) {
-  // the queries' workgroups, as launch_rows has them
+  // the queries' workgroups, as launch_rows has them: four tokens each where the call has
+  // tokens enough (40 heads of 128: 16 sequences of 1024 tokens 80 us against 88 with one, 64
+  // of 32 20 against 28; one of 1024 9.8 against 9.4), and not where a sequence has fewer
   const int groups = head_groups(a, 0);
-  const int n_tok = max_q >= 2048 ? kTurnTokens : 1;
+  const int n_tok = max_q >= kTurnTokens && std::min(x.rows, (int64_t)max_q * s.B) >= 2048 ? kTurnTokens : 1;
   const int per_wg = n_tok == 1 && groups > BS / 64 && (int64_t)max_q * s.B * groups < 8192 ? BS / 64 : groups;
   const uint32_t q_blocks =
       groups ? (uint32_t)((max_q + n_tok - 1) / n_tok * ((groups + per_wg - 1) / per_wg)) : 0;

@@ -106,3 +106,33 @@ def test_frequencies_changed_before_the_backward_pass(lib):  # noqa: F811
     same_bits(torch.autograd.grad(out.sum(), q)[0], want)
     plain = RotateHeads(64, None)                 # no rotation: nothing to change
     torch.autograd.grad(plain(q, pos).sum(), q)
+
+
+@pytest.mark.parametrize("P,D,pairs,inter", [(16, 64, 32, False), (64, 128, 64, True), (32, 80, 10, False),
+                                             (128, 256, 128, False)])
+def test_many_queries_of_short_sequences(lib, P, D, pairs, inter):  # noqa: F811
+    """Calls of thousands of rows, none of whose sequences is long: bit for bit rotate_heads and
+    cache_write, rows behind the sequences left as they are, whatever bound max_new is."""
+    say("many queries", P, D, pairs, inter)
+    H, G, dt, g = 1, 3, torch.bfloat16, gen(P + D)
+    new = [0, 1, 2, 3, 4, 5, 7, 130] + torch.randint(1, 60, (90,), generator=g).tolist()
+    lens = [n + (i % 3) * 9 for i, n in enumerate(new)]
+    B, T, per = len(new), sum(new), -(-max(lens) // P)
+    assert T > 2048
+    rot = lib.Rotary(freqs_of(pairs).cuda(), interleaved=inter)
+    w = (1 + 0.3 * torch.randn(D, generator=g)).to(dt).cuda()
+    q, k, v = torch.randn((T, H * (G + 2), D), generator=g).to(dt).cuda().split([H * G, H, H], dim=1)
+    table = torch.arange(B * per, dtype=torch.int32, device="cuda").view(B, per)
+    length, cu, pos = ints(lens), cu_of(new), positions_of(lens, new).cuda()
+    a = blank_cache(lib, B * per, B, H, D, P, dt)
+    q1, k1 = lib.rotate_heads(q, pos, rot, k=k, q_weight=w, k_weight=w)
+    lib.cache_write(a, k1, v, table, length, cu=cu, max_new=130)
+    for most in (130, None):
+        b = blank_cache(lib, B * per, B, H, D, P, dt)
+        out = torch.full((T + 3, H * G, D), 9.0, dtype=dt, device="cuda")
+        lib.cache_append(b, k, v, table, length, q=q, rotary=rot, q_weight=w, k_weight=w, cu=cu, max_new=most,
+                         q_out=out[:T])
+        same_bits(out[:T], q1, "queries")
+        assert bool((out[T:] == 9).all())
+        for x, y in zip(parts_of(a), parts_of(b)):
+            assert torch.equal(x, y)
