@@ -152,10 +152,11 @@ class _RotateHeadsFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, positions, rotary, q_weight, k_weight, eps):
         out = _rotate_heads(q, positions, rotary, k=k, q_weight=q_weight, k_weight=k_weight, eps=eps)
+        # (frequencies made in inference mode have no version to compare, and are not saved)
+        freqs = None if rotary is None or rotary.freqs.is_inference() else rotary.freqs
         # without a norm the gradient does not depend on what went in
         ctx.save_for_backward(positions, q if q_weight is not None else None,
-                              k if k_weight is not None else None, q_weight, k_weight,
-                              None if rotary is None else rotary.freqs)
+                              k if k_weight is not None else None, q_weight, k_weight, freqs)
         ctx.rotary, ctx.eps, ctx.two = rotary, eps, k is not None
         return out
 
@@ -164,7 +165,7 @@ class _RotateHeadsFn(torch.autograd.Function):
     def backward(ctx, *grads):
         positions, q, k, q_weight, k_weight, freqs = ctx.saved_tensors
         rotary = ctx.rotary
-        if rotary is not None and freqs.data_ptr() != rotary.freqs.data_ptr():   # (kept elsewhere by a hook)
+        if freqs is not None and freqs.data_ptr() != rotary.freqs.data_ptr():   # (kept elsewhere by a hook)
             rotary = type(rotary)(freqs, rotary.interleaved, rotary.factor)
         dq, dk, dqw, dkw = _rotate_heads_backward(
             _whole(grads[0]), positions, rotary, q=q,

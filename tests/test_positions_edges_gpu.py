@@ -286,3 +286,16 @@ def test_shared_trees_with_any_mask(lib, case, dtype):  # noqa: F811
             one = slice(at, at + n)
             check_tree(lib, cache, table, slots, kv[b:b + 1], lens[b:b + 1], None, q[one], k[one], v[one], P, dt,
                        0.11, 0, None, got[one], [0] * n, cut)
+
+
+def test_frequencies_made_in_inference_mode_train(lib):  # noqa: F811
+    """Frequencies that carry no version (autograd saves no such tensor) serve in training too."""
+    from mixed_precision_quantized_int8_amd.module import RotateHeads
+
+    with torch.inference_mode():
+        rot = lib.rotary(64)
+    q = torch.randn((5, 2, 64), generator=gen(1)).half().cuda().requires_grad_()
+    pos = ints(list(range(5)))
+    got, want = (torch.autograd.grad(RotateHeads(64, r)(q, pos).float().square().sum(), q)[0]
+                 for r in (rot, lib.rotary(64)))
+    same_bits(got, want)
