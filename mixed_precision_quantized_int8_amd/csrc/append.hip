@@ -210,19 +210,21 @@ namespace {
 template <bool BF, int LAYOUT, int BS, int NU>
 void launch_sized(const Cache& c, const Sequences& s, const CacheRows& x, const HeadArgs& a,
                   const uint16_t* k_w, uint32_t page_blocks, int max_q, hipStream_t stream) {
-  // The queries' workgroups, as launch_rows has them: a token each, or four where the call has
-  // tokens enough for 2048 waves of them, each with at most eight groups of heads one after the
-  // other, four with a workgroup of one wave or two (40 heads of 128, pages of 64: 16
-  // sequences of 1024 tokens 80 us against 88 with one, 64 of 32 20 against 28; pages of 16,
-  // where a workgroup is one wave and would have 16 groups, 87 against 78 and 22 against 14),
-  // or where the bound is loose, so that most workgroups have nothing to do (256 sequences of
-  // 20 tokens, bounded by their sum: 251 us against 847).
+  // The queries' workgroups, as launch_rows has them: a token each, or four where that leaves
+  // waves enough and each of them at most eight groups of heads one after the other (40 heads
+  // of 128, pages of 64: 16 sequences of 1024 tokens 80 us against 88 with one, 64 of 32 20
+  // against 28; pages of 16, where a workgroup is one wave and would have 16 groups, 87
+  // against 78 and 22 against 14; of 32, eight groups on two waves, 81 against 81, a quarter
+  // of 80 turned 112 against 123, 64 sequences of 64 27 against 24), or where the bound is
+  // loose, so that most workgroups have nothing to do (256 sequences of 20 tokens, bounded by
+  // their sum: 251 us against 847).
   constexpr int kWaves = BS / 64;
-  const int groups = head_groups(a, 0);
+  const int groups = head_groups(a, 0), each = (kTurnTokens * groups + kWaves - 1) / kWaves;
   const int64_t bound = (int64_t)max_q * s.B, rows = std::min(x.rows, bound);
+  const int64_t waves = rows / kTurnTokens * kWaves;
   const bool four = max_q >= kTurnTokens &&
                     (bound > 2 * rows ? rows >= 2048
-                                      : rows * kWaves >= 8192 && groups <= (kWaves == 4 ? 8 : kWaves));
+                                      : each <= 8 && waves >= (each <= 4 || kWaves == 4 ? 2048 : 4096));
   const int n_tok = four ? kTurnTokens : 1;
   const int per_wg = n_tok == 1 && groups > BS / 64 && (int64_t)max_q * s.B * groups < 8192 ? BS / 64 : groups;
   const uint32_t q_blocks =
