@@ -434,8 +434,8 @@ i8l_status int8_cache_attention(const i8l_kv_cache *cache, const i8l_sequences *
  * Rotary positions with the norm of each query and key head, on rows and on the way
  * into the cache; attention for trees of drafted tokens behind the cached ones. */
 
-/* Rotary positions: pair i of a head at position p turns by the angle p * freqs[i]
- * (formed in 64 bits), f = factor:
+/* Rotary positions: pair i of a head at position p turns by the angle p * freqs[i] (its
+ * fraction of a turn is formed to 2^-25, in 64 bits past 2^20 turns), f = factor:
  *   y_a = f (x_a cos - x_b sin),  y_b = f (x_a sin + x_b cos),
  * pairs (a, b) = (i, i + pairs), or (2 i, 2 i + 1) if interleaved; elements from
  * 2 * pairs on stay.  pairs 0 (freqs may be NULL): nothing turns. */

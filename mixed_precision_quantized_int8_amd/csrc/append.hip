@@ -170,9 +170,13 @@ __device__ __forceinline__ void append_keys(const Cache& c, const Sequences& s, 
   }
 }
 
-// (80 registers, for six waves a SIMD: 24.8 k tokens, 32 heads on 8, 132 us, with 93
-// registers 137; keys kept in registers as values are, 126 of them, 148.  Halves through
-// LDS do not fit.)
+// (Pages of up to 8192 elements, NU 1: 80 registers, for six waves a SIMD: 24.8 k tokens, 32
+// heads on 8, 132 us, with 93 registers 137; keys kept in registers as values are, 126 of
+// them, 148.  Larger pages hold more: NU 2 92 - 101 registers and 32 KB of LDS, four waves,
+// NU 4 64 KB, two; queries share the launch and have no more.  8192 tokens, 8 heads: of 128
+// on 32 41.6 us with pages of 64 (NU 1), 42.0 of 128 (2); of 256 on 8 51.3 with pages of 32,
+// 53.5 of 64 (2), 65.0 of 128 (4).  Halves through LDS do not fit: 132 - 160 registers,
+// three waves, one with NU 4.)
 template <bool BF, int LAYOUT, int BS, int NU>
 __global__ __launch_bounds__(BS) __attribute__((amdgpu_waves_per_eu(LAYOUT == kTurnOdd ? 2 : 6)))
 void cache_append_kernel(Cache c, Sequences s, CacheRows x, HeadArgs a, const uint16_t* k_w,

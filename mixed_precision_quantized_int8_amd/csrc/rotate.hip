@@ -193,7 +193,7 @@ void launch_forward(const HeadArgs& a, hipStream_t stream) {
 
 // (333 tokens 13.3 us with one a workgroup against 15.8 with four, 1024 tokens 24.7 against 17.6)
 int grad_tokens(int rows) { return rows >= 768 ? kTurnTokens : 1; }
-// At most four workgroups a compute unit: their rows of partial sums are read again.
+// At most four workgroups a compute unit and side: their rows of partial sums are read again.
 int grad_blocks(int rows) {
   const int n = grad_tokens(rows), blocks = (int)(((int64_t)rows + n - 1) / n);
   return blocks < 1 ? 1 : blocks > 1024 ? 1024 : blocks;

@@ -155,7 +155,9 @@ class Int8DecoderLayer(torch.nn.Module):
 
     def _answers(self, q, cu):
         """Where attention writes.  With cu there may be rows that it leaves as they are; the
-        next product's outlier columns are those of all of its rows, so these hold 0."""
+        next product's outlier columns are those of all of its rows, so these hold 0 (a
+        launch: 3 us of 145 or 209 for 16 x 8 rows, with and without ``codes``, 4 of 575 or
+        745 for 2048, 10 of 1780 or 2220 for 8192; sizes as above)."""
         return None if cu is None else q.new_zeros(q.shape)
 
     def _rest(self, a, r):

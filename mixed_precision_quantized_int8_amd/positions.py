@@ -93,8 +93,10 @@ def rotary(dim, base=10000.0, interleaved=False, scaling=None, scale=1.0, origin
       "base"    base * scale ** (dim / (dim - 2)): the slowest pair over scale, the
                 fastest as it was;
       "parts"   by the turns r_i that a pair makes over ``original`` tokens: those below
-                ``low`` over scale, those above ``high`` as they were, between them a ramp;
-                ``factor`` then defaults to 1 + 0.1 ln(scale).
+                ``low`` over scale, those above ``high`` as they were, between them a ramp
+                that is linear in r_i (one in the pair's number, as some models have, is
+                given to ``Rotary`` as frequencies); ``factor`` then defaults to
+                1 + 0.1 ln(scale).
     """
     if dim < 0 or dim % 2:
         raise ValueError(f"dim must be even and at least 0, got {dim}")

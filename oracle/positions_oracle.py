@@ -58,7 +58,8 @@ def rotate(x, positions, freqs, interleaved=False, factor=1.0, weight=None, eps=
     quotient, three products), 8 in an angle's sine and cosine (a turn's fraction is within
     2^-25, 3.2 of them after the factor 2 pi, the functions within 1.3e-7, 2.2 of them, the
     factor one), 3 in the pair's products and sum: below 2^-19 of what the element is made
-    of.  The angle itself, formed in 64 bits, errs by 3 roundings of 2^-53 of its size."""
+    of.  Past 2^20 turns the angle is formed in 64 bits: 3 roundings of 2^-53 of its size
+    (below, its fraction in two 32-bit parts is within the 2^-25 above)."""
     d = x.to(F64)
     w = None if weight is None else weight.to(F64)
     n = norm(d, w, eps)
